@@ -10,6 +10,7 @@
 #include <mutex>
 #include <vector>
 
+#include "cache8.cuh"
 #include "kernels.h"
 #include "sfa.h"
 
@@ -453,6 +454,222 @@ sfa_status sfa_decode_attn(const sfa_shape* shape, const void* q, const void* K_
   p.o = o; p.lse = lse; p.status = status_word;
   p.scale = scale > 0.f ? scale : (float)(1.0 / sqrt((double)shape->head_dim));
   return cuda_status(launch_decode_attn(p, as_stream(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// 8-bit KV cache
+// ---------------------------------------------------------------------------
+namespace {
+
+// Shape and block rules of the sfa_cache8_* calls; `any_heads` for the calls that read no q.
+sfa_status check_cache8(const sfa_shape* shape, int block, bool any_heads) {
+  if (shape == nullptr) return SFA_ERR_INVALID_ARG;
+  sfa_shape s = *shape;
+  if (any_heads) s.heads_q = s.heads_kv;
+  const sfa_status st = check_decode_shape(&s);
+  if (st != SFA_OK) return st;
+  if (block != 64 && block != 128) return SFA_ERR_SHAPE;
+  return SFA_OK;
+}
+
+sfa_status check_cache8_arrays(const sfa_cache8* c) {
+  if (c->k == nullptr || c->v == nullptr || c->k_scale == nullptr || c->v_scale == nullptr || c->lens == nullptr)
+    return SFA_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v)) return SFA_ERR_INVALID_ARG;
+  return SFA_OK;
+}
+
+struct Cache8Ws {
+  size_t ml, o, lse2, scores, total;
+};
+
+// Pieces of the split attention: one per CTA and unit cut at most (cache8.cuh).
+int cache8_ctas(const sfa_shape* s) {
+  const long long tiles = (long long)s->batch * s->heads_kv * ((s->seq_len + c8::kTile - 1) / c8::kTile);
+  return (int)(tiles < c8::kMaxCtas ? tiles : c8::kMaxCtas);
+}
+
+int cache8_row(const sfa_shape* s) { return (s->seq_len + 127) / 128 * 128; }
+
+sfa_status cache8_cols(const sfa_shape* s, int nq, int* cols) {
+  if (nq < 1) return SFA_ERR_INVALID_ARG;
+  const long long c = (long long)nq * (s->heads_q / s->heads_kv);
+  if (c > c8::kMaxCols || (long long)s->batch * s->heads_kv * c >= (1LL << 31)) return SFA_ERR_UNSUPPORTED;
+  *cols = (int)c;
+  return SFA_OK;
+}
+
+Cache8Ws cache8_ws(const sfa_shape* s, int cols, bool weights) {
+  const size_t units = (size_t)s->batch * s->heads_kv, slots = units + cache8_ctas(s);
+  Cache8Ws w;
+  w.ml = 0;
+  w.o = align256(w.ml + slots * cols * 2 * sizeof(float));
+  w.lse2 = align256(w.o + slots * cols * s->head_dim * sizeof(float));
+  w.scores = align256(w.lse2 + units * cols * sizeof(float));
+  w.total = align256(w.scores + (weights ? units * cols * (size_t)cache8_row(s) * sizeof(float) : 0));
+  return w;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  if (a == nullptr || b == nullptr) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+void cache8_fill(const sfa_shape* s, const sfa_cache8* c, Cache8Attn* p) {
+  memset(p, 0, sizeof(*p));
+  p->k = static_cast<const uint8_t*>(c->k);
+  p->v = static_cast<const uint8_t*>(c->v);
+  p->ks = c->k_scale;
+  p->vs = c->v_scale;
+  p->lens = c->lens;
+  p->B = s->batch; p->Hq = s->heads_q; p->Hkv = s->heads_kv; p->L = s->seq_len; p->D = s->head_dim;
+  p->T = c->block;
+  p->nblk = (s->seq_len + c->block - 1) / c->block;
+}
+
+}  // namespace
+
+extern "C" {
+
+sfa_status sfa_cache8_append(const sfa_shape* shape, const sfa_cache8* cache, const void* K_new, const void* V_new,
+                             int n, const int32_t* at, const int32_t* counts, int* status_word, void* stream) {
+  if (cache == nullptr) return SFA_ERR_INVALID_ARG;
+  sfa_status st = check_cache8(shape, cache->block, true);
+  if (st == SFA_OK) st = check_cache8_arrays(cache);
+  if (st != SFA_OK) return st;
+  if (K_new == nullptr || V_new == nullptr || n < 1 || !aligned16(K_new) || !aligned16(V_new))
+    return SFA_ERR_INVALID_ARG;
+  const size_t nb = (size_t)shape->batch * sizeof(int32_t);
+  if (overlap(at, nb, cache->lens, nb) || overlap(counts, nb, cache->lens, nb)) return SFA_ERR_INVALID_ARG;
+  Cache8Append p;
+  p.K = K_new; p.V = V_new;
+  p.k = static_cast<uint8_t*>(cache->k); p.v = static_cast<uint8_t*>(cache->v);
+  p.ks = cache->k_scale; p.vs = cache->v_scale; p.weight = cache->weight;
+  p.at = at != nullptr ? at : cache->lens;
+  p.counts = counts; p.lens = cache->lens; p.status = status_word;
+  p.B = shape->batch; p.Hkv = shape->heads_kv; p.L = shape->seq_len; p.D = shape->head_dim;
+  p.T = cache->block; p.n = n;
+  p.nblk = (p.L + p.T - 1) / p.T;
+  p.in_place = at == nullptr;
+  return cuda_status(launch_cache8_append(p, as_stream(stream)));
+}
+
+size_t sfa_cache8_attn_workspace(const sfa_shape* shape, int nq, int weights) {
+  int cols = 0;
+  if (check_cache8(shape, 128, false) != SFA_OK || cache8_cols(shape, nq, &cols) != SFA_OK) return 0;
+  return cache8_ws(shape, cols, weights != 0).total;
+}
+
+sfa_status sfa_cache8_attn(const sfa_shape* shape, const sfa_cache8* cache, const void* q, int nq, int back,
+                           float scale, void* o, float* lse, const float* weight_in, float* weight_out,
+                           void* workspace, size_t workspace_bytes, int* status_word, void* stream) {
+  if (cache == nullptr) return SFA_ERR_INVALID_ARG;
+  sfa_status st = check_cache8(shape, cache->block, false);
+  if (st == SFA_OK) st = check_cache8_arrays(cache);
+  int cols = 0;
+  if (st == SFA_OK) st = cache8_cols(shape, nq, &cols);
+  if (st != SFA_OK) return st;
+  if (q == nullptr || o == nullptr || back < 0 || !isfinite(scale) || !aligned16(q)) return SFA_ERR_INVALID_ARG;
+  if (weight_in != nullptr && weight_out == nullptr) return SFA_ERR_INVALID_ARG;
+  const Cache8Ws w = cache8_ws(shape, cols, weight_out != nullptr);
+  if (workspace == nullptr || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return SFA_ERR_WORKSPACE;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  Cache8Attn p;
+  cache8_fill(shape, cache, &p);
+  p.q = q; p.o = o; p.lse = lse; p.w_in = weight_in; p.w_out = weight_out; p.status = status_word;
+  p.part_ml = reinterpret_cast<float*>(ws + w.ml);
+  p.part_o = reinterpret_cast<float*>(ws + w.o);
+  p.lse2 = reinterpret_cast<float*>(ws + w.lse2);
+  p.scores = weight_out != nullptr ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
+  p.nq = nq; p.cols = cols; p.back = back; p.G = cache8_ctas(shape); p.Lp = cache8_row(shape);
+  p.sl2 = (scale > 0.f ? scale : (float)(1.0 / sqrt((double)shape->head_dim))) * 1.4426950408889634f;
+  return cuda_status(launch_cache8_attn(p, as_stream(stream)));
+}
+
+sfa_status sfa_cache8_attn_list(const sfa_shape* shape, const sfa_cache8* cache, const void* q, const int* idx, int k,
+                                float scale, void* o, float* lse, int* status_word, void* stream) {
+  if (cache == nullptr) return SFA_ERR_INVALID_ARG;
+  sfa_status st = check_cache8(shape, cache->block, false);
+  if (st == SFA_OK) st = check_cache8_arrays(cache);
+  if (st != SFA_OK) return st;
+  if (q == nullptr || idx == nullptr || o == nullptr || k < 1 || !isfinite(scale) || !aligned16(q))
+    return SFA_ERR_INVALID_ARG;
+  Cache8Attn p;
+  cache8_fill(shape, cache, &p);
+  p.q = q; p.idx = idx; p.k_list = k; p.o = o; p.lse = lse; p.status = status_word;
+  p.sl2 = (scale > 0.f ? scale : (float)(1.0 / sqrt((double)shape->head_dim))) * 1.4426950408889634f;
+  return cuda_status(launch_cache8_attn_list(p, as_stream(stream)));
+}
+
+size_t sfa_cache8_evict_workspace(const sfa_shape* shape, int keep) {
+  if (keep < 1 || check_cache8(shape, 128, true) != SFA_OK) return 0;
+  return align256((size_t)shape->batch * shape->heads_kv * keep * sizeof(int));
+}
+
+sfa_status sfa_cache8_evict(const sfa_shape* shape, const sfa_cache8* src, const sfa_cache8* dst, int dst_len,
+                            int keep, int recent, int* idx, void* workspace, size_t workspace_bytes,
+                            int* status_word, void* stream) {
+  if (src == nullptr || dst == nullptr) return SFA_ERR_INVALID_ARG;
+  sfa_status st = check_cache8(shape, src->block, true);
+  if (st == SFA_OK) st = check_cache8_arrays(src);
+  if (st == SFA_OK) st = check_cache8_arrays(dst);
+  if (st != SFA_OK) return st;
+  if (dst->block != src->block) return SFA_ERR_SHAPE;
+  if (src->weight == nullptr || keep < 1 || recent < 0 || recent > keep || dst_len < keep) return SFA_ERR_INVALID_ARG;
+  const size_t units = (size_t)shape->batch * shape->heads_kv;
+  if ((long long)units * dst_len >= (1LL << 31)) return SFA_ERR_UNSUPPORTED;
+  const size_t rows = units * shape->seq_len * shape->head_dim, drows = units * (size_t)dst_len * shape->head_dim;
+  const size_t nblk = (shape->seq_len + src->block - 1) / src->block, dnblk = (dst_len + src->block - 1) / src->block;
+  const void* a[6] = {src->k, src->v, src->k_scale, src->v_scale, src->lens, src->weight};
+  const size_t na[6] = {rows, rows, units * nblk * 4, units * nblk * 4, (size_t)shape->batch * 4,
+                        units * shape->seq_len * 4};
+  const void* d[6] = {dst->k, dst->v, dst->k_scale, dst->v_scale, dst->lens, dst->weight};
+  const size_t nd[6] = {drows, drows, units * dnblk * 4, units * dnblk * 4, (size_t)shape->batch * 4,
+                        units * (size_t)dst_len * 4};
+  for (int i = 0; i < 6; ++i)
+    for (int j = 0; j < 6; ++j)
+      if (overlap(a[i], na[i], d[j], nd[j])) return SFA_ERR_INVALID_ARG;
+  if (idx == nullptr) {
+    if (workspace == nullptr || workspace_bytes < sfa_cache8_evict_workspace(shape, keep) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255))
+      return SFA_ERR_WORKSPACE;
+    idx = static_cast<int*>(workspace);
+  }
+  Cache8Evict p;
+  p.k = static_cast<const uint8_t*>(src->k); p.v = static_cast<const uint8_t*>(src->v);
+  p.ks = src->k_scale; p.vs = src->v_scale; p.lens = src->lens; p.weight = src->weight;
+  p.dk = static_cast<uint8_t*>(dst->k); p.dv = static_cast<uint8_t*>(dst->v);
+  p.dks = dst->k_scale; p.dvs = dst->v_scale; p.dlens = dst->lens; p.dweight = dst->weight;
+  p.idx = idx; p.status = status_word;
+  p.B = shape->batch; p.Hkv = shape->heads_kv; p.L = shape->seq_len; p.D = shape->head_dim; p.T = src->block;
+  p.nblk = (int)nblk; p.dL = dst_len; p.dnblk = (int)dnblk; p.keep = keep; p.recent = recent;
+  return cuda_status(launch_cache8_evict(p, as_stream(stream)));
+}
+
+sfa_status sfa_cache8_fc_gather(const sfa_shape* shape, const sfa_cache8* cache, const int* fc, int nfc, int pos0,
+                                int npos, void* K_fc, void* stream) {
+  if (cache == nullptr) return SFA_ERR_INVALID_ARG;
+  sfa_status st = check_cache8(shape, cache->block, true);
+  if (st != SFA_OK) return st;
+  if (cache->k == nullptr || cache->k_scale == nullptr || fc == nullptr || K_fc == nullptr) return SFA_ERR_INVALID_ARG;
+  if (!aligned16(cache->k) || !aligned16(K_fc)) return SFA_ERR_INVALID_ARG;
+  sfa_shape s = *shape;
+  s.heads_q = s.heads_kv;
+  DecodeParams d;
+  st = decode_params(&s, fc, nfc, &d);
+  if (st != SFA_OK) return st;
+  if (pos0 < 0 || npos < 0 || (long long)pos0 + npos > shape->seq_len) return SFA_ERR_INVALID_ARG;
+  Cache8Gather p;
+  p.k = static_cast<const uint8_t*>(cache->k); p.ks = cache->k_scale; p.out = K_fc;
+  p.B = d.B; p.Hkv = d.Hkv; p.L = d.L; p.D = d.D; p.T = cache->block;
+  p.nblk = (d.L + cache->block - 1) / cache->block;
+  p.nfc = nfc; p.pos0 = pos0; p.npos = npos;
+  memcpy(p.fc, d.fc, sizeof(p.fc));
+  return cuda_status(launch_cache8_gather(p, as_stream(stream)));
 }
 
 }  // extern "C"

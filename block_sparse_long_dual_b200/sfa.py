@@ -43,6 +43,11 @@ class Rope(ctypes.Structure):
     _fields_ = [("cos", c_void_p), ("sin", c_void_p), ("apply", c_int32)]
 
 
+class Cache8(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p), ("lens", c_void_p),
+                ("weight", c_void_p), ("block", c_int32)]
+
+
 _lib = None
 
 
@@ -91,6 +96,25 @@ def load() -> ctypes.CDLL:
     lib.sfa_decode_attn.restype = c_int
     lib.sfa_decode_attn.argtypes = [POINTER(Shape), c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_float,
                                     c_void_p, c_void_p, c_void_p, c_void_p]
+    c8 = POINTER(Cache8)
+    lib.sfa_cache8_append.restype = c_int
+    lib.sfa_cache8_append.argtypes = [POINTER(Shape), c8, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p,
+                                      c_void_p]
+    lib.sfa_cache8_attn_workspace.restype = c_size_t
+    lib.sfa_cache8_attn_workspace.argtypes = [POINTER(Shape), c_int, c_int]
+    lib.sfa_cache8_attn.restype = c_int
+    lib.sfa_cache8_attn.argtypes = [POINTER(Shape), c8, c_void_p, c_int, c_int, c_float, c_void_p, c_void_p, c_void_p,
+                                    c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]
+    lib.sfa_cache8_attn_list.restype = c_int
+    lib.sfa_cache8_attn_list.argtypes = [POINTER(Shape), c8, c_void_p, c_void_p, c_int, c_float, c_void_p, c_void_p,
+                                         c_void_p, c_void_p]
+    lib.sfa_cache8_evict_workspace.restype = c_size_t
+    lib.sfa_cache8_evict_workspace.argtypes = [POINTER(Shape), c_int]
+    lib.sfa_cache8_evict.restype = c_int
+    lib.sfa_cache8_evict.argtypes = [POINTER(Shape), c8, c8, c_int, c_int, c_int, c_void_p, c_void_p, c_size_t,
+                                     c_void_p, c_void_p]
+    lib.sfa_cache8_fc_gather.restype = c_int
+    lib.sfa_cache8_fc_gather.argtypes = [POINTER(Shape), c8, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p]
     lib.sfa_selftest_bounded_wait.restype = c_int
     lib.sfa_selftest_bounded_wait.argtypes = [c_void_p, ctypes.c_uint, c_int, c_void_p]
     _lib = lib
@@ -591,7 +615,9 @@ class FasaDecode:
     focused attention.  ``fc`` [Hkv, nfc] are the dominant pairs (an input: the offline
     calibration that finds them is not part of this library).  Buffers are allocated once;
     ``refresh_keys`` (re)builds the compact key copy for a position range, ``__call__`` runs
-    the step's three kernels."""
+    the step's three kernels.  Wherever a key (and value) cache is taken, a ``KvCache8`` of
+    capacity ``seq_len`` may be given instead as ``K_cache`` (``V_cache`` left None): the
+    compact copy and the attention then read the 8-bit cache."""
 
     def __init__(self, *, batch, heads_q, heads_kv, seq_len, head_dim, fc, k, device="cuda", with_lse=True):
         self.fc = fc
@@ -610,27 +636,38 @@ class FasaDecode:
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
 
     def refresh_keys(self, K_cache, pos0=0, npos=None, stream=None):
+        if isinstance(K_cache, KvCache8):
+            cache8_fc_gather(K_cache, self.fc, K_fc=self.K_fc, pos0=pos0, npos=npos, stream=stream)
+            return
         decode_fc_gather(K_cache, self.fc, K_fc=self.K_fc, pos0=pos0, npos=npos, stream=stream)
 
     def select(self, q, stream=None):
         decode_select(q, self.K_fc, self.fc, self.shape.seq_len, k=self.k, idx=self.idx, workspace=self.workspace,
                       status=self.status, stream=stream)
 
-    def attend(self, q, K_cache, V_cache, stream=None):
+    def attend(self, q, K_cache, V_cache=None, stream=None):
+        if isinstance(K_cache, KvCache8):
+            cache8_attn_list(q, K_cache, self.idx, o=self.o, lse=self.lse, status=self.status, stream=stream)
+            return
         decode_attn(q, K_cache, V_cache, self.idx, o=self.o, lse=self.lse, status=self.status, stream=stream)
 
-    def __call__(self, q, K_cache, V_cache, stream=None):
+    def __call__(self, q, K_cache, V_cache=None, stream=None):
         self.select(q, stream)
         self.attend(q, K_cache, V_cache, stream)
         return self.o
 
-    def step(self, q, K_cache, V_cache, pos: int):
+    def step(self, q, K_cache, V_cache=None, pos: int = -1):
         """One decode step for the token at position ``pos`` (its compact key row, select, attend)
         replayed as a CUDA graph: captured on the first call for these buffers and this position,
         replayed on later calls (new values in the same q / cache tensors are picked up; the
         kernels, their arguments and the buffers are fixed at capture).  Runs on the current
         stream; returns ``self.o``."""
-        key = (q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), int(pos))
+        if pos < 0:
+            raise ValueError("step() needs the position of the newest token")
+        if isinstance(K_cache, KvCache8):
+            key = (q.data_ptr(), K_cache.k.data_ptr(), K_cache.v.data_ptr(), K_cache.lens.data_ptr(), int(pos))
+        else:
+            key = (q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), int(pos))
         if getattr(self, "_graph_key", None) != key:
             side = torch.cuda.Stream(q.device)
             side.wait_stream(torch.cuda.current_stream(q.device))
@@ -645,6 +682,212 @@ class FasaDecode:
             self._graph, self._graph_key = graph, key
         self._graph.replay()
         return self.o
+
+
+# ---------------------------------------------------------------------------
+# 8-bit KV cache: e4m3 codes with a power-of-two scale per block of tokens and head
+# ---------------------------------------------------------------------------
+class KvCache8:
+    """Keys and values of ``B`` sequences in 8 bits (sfa_cache8 of include/sfa.h).
+
+    ``k``, ``v`` [B, Hkv, capacity, d] float8_e4m3fn codes; ``k_scale``, ``v_scale``
+    [B, Hkv, ceil(capacity / block)] float32 powers of two (value = code * scale); ``lens`` [B]
+    int32 valid tokens; ``weight`` [B, Hkv, capacity] float32 attention weight received so far
+    (None: not kept).  The tensors are checked once here and must not be replaced afterwards
+    (their contents may change).  ``KvCache8.empty`` allocates them.  ``status`` is the device
+    word that the methods report errors found on the device to."""
+
+    def __init__(self, *, k, v, k_scale, v_scale, lens, weight=None, block=128):
+        if k.dim() != 4:
+            raise ValueError("k must be [B, Hkv, capacity, d]")
+        B, Hkv, cap, d = k.shape
+        nblk = -(-cap // block) if block > 0 else 0
+        _cuda(k, "k")
+        _expect(k, "k", k.shape, torch.float8_e4m3fn)
+        _expect(v, "v", k.shape, torch.float8_e4m3fn, k.device)
+        _expect(k_scale, "k_scale", (B, Hkv, nblk), torch.float32, k.device)
+        _expect(v_scale, "v_scale", (B, Hkv, nblk), torch.float32, k.device)
+        _expect(lens, "lens", (B,), torch.int32, k.device)
+        _expect(weight, "weight", (B, Hkv, cap), torch.float32, k.device)
+        self.k, self.v, self.k_scale, self.v_scale, self.lens, self.weight = k, v, k_scale, v_scale, lens, weight
+        self.batch, self.heads_kv, self.capacity, self.head_dim, self.block = B, Hkv, cap, d, block
+        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._c = Cache8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), lens.data_ptr(),
+                         None if weight is None else weight.data_ptr(), block)
+        self._shapes = {}
+        self._workspaces = {}
+
+    @classmethod
+    def empty(cls, *, batch, heads_kv, capacity, head_dim, block=128, weight=True, device="cuda"):
+        """A cache with no tokens in it."""
+        dev = torch.device(device)
+        nblk = -(-capacity // block)
+        kw = dict(device=dev)
+        return cls(k=torch.zeros((batch, heads_kv, capacity, head_dim), dtype=torch.float8_e4m3fn, **kw),
+                   v=torch.zeros((batch, heads_kv, capacity, head_dim), dtype=torch.float8_e4m3fn, **kw),
+                   k_scale=torch.ones((batch, heads_kv, nblk), **kw), v_scale=torch.ones((batch, heads_kv, nblk), **kw),
+                   lens=torch.zeros((batch,), dtype=torch.int32, **kw),
+                   weight=torch.zeros((batch, heads_kv, capacity), **kw) if weight else None, block=block)
+
+    def shape(self, heads_q: int) -> Shape:
+        s = self._shapes.get(heads_q)
+        if s is None:
+            s = self._shapes[heads_q] = Shape(self.batch, heads_q, self.heads_kv, self.capacity, self.head_dim, BF16)
+        return s
+
+    def _workspace(self, q, weights):
+        """The handle's own attention workspace for queries like q (one per shape, made on first use)."""
+        key = (q.shape[1], q.shape[2] if q.dim() == 4 else 1, weights)
+        if key not in self._workspaces:
+            self._workspaces[key] = torch.empty(cache8_attn_workspace(q, self, weights=weights), dtype=torch.uint8,
+                                                device=self.k.device)
+        return self._workspaces[key]
+
+    def append(self, K, V, *, at=None, counts=None, stream=None):
+        """Quantise K, V [B, Hkv, n, d] bf16 in at ``at`` (default: behind the tokens held); see cache8_append."""
+        cache8_append(self, K, V, at=at, counts=counts, status=self.status, stream=stream)
+
+    def attend(self, q, *, back=0, scale=0.0, accumulate=False, o=None, lse=None, stream=None):
+        """Attention of q [B, Hq, d] or [B, Hq, nq, d] over the whole cache; ``accumulate`` adds the
+        attention weights to ``weight``.  Uses the handle's workspace: calls that overlap on the GPU (other
+        streams, captured graphs replayed together) need cache8_attn with a workspace each."""
+        if accumulate and self.weight is None:
+            raise ValueError("accumulate needs a cache with weights")
+        w = self.weight if accumulate else None
+        return cache8_attn(q, self, back=back, scale=scale, o=o, lse=lse, weight_in=w, weight_out=w,
+                           workspace=self._workspace(q, accumulate), status=self.status, stream=stream)
+
+    def attend_list(self, q, idx, *, scale=0.0, o=None, lse=None, stream=None):
+        """Attention of q [B, Hq, d] over the tokens of idx [B, Hq, k]; see cache8_attn_list."""
+        return cache8_attn_list(q, self, idx, scale=scale, o=o, lse=lse, status=self.status, stream=stream)
+
+    def evict(self, dst: "KvCache8", *, keep, recent=0, idx=None, stream=None):
+        """Move the tokens worth keeping to ``dst`` (see cache8_evict); returns their rows here."""
+        return cache8_evict(self, dst, keep=keep, recent=recent, idx=idx, status=self.status, stream=stream)
+
+
+def cache8_append(cache: KvCache8, K, V, *, at=None, counts=None, status=None, stream=None):
+    """sfa_cache8_append: rows K, V [B, Hkv, n, d] bf16 into the cache at positions ``at`` [B] int32
+    (None: at cache.lens), the first ``counts`` [B] int32 of them (None: all)."""
+    lib = load()
+    if K.dim() != 4:
+        raise ValueError("K must be [B, Hkv, n, d]")
+    n = K.shape[2]
+    dev = cache.k.device
+    rows = (cache.batch, cache.heads_kv, n, cache.head_dim)
+    _expect(K, "K", rows, torch.bfloat16, dev)
+    _expect(V, "V", rows, torch.bfloat16, dev)
+    _expect(at, "at", (cache.batch,), torch.int32, dev)
+    _expect(counts, "counts", (cache.batch,), torch.int32, dev)
+    _status(status)
+    _check(lib.sfa_cache8_append(ctypes.byref(cache.shape(cache.heads_kv)), ctypes.byref(cache._c), _ptr(K), _ptr(V),
+                                 n, _ptr(at), _ptr(counts), _ptr(status), _stream(stream)), "sfa_cache8_append")
+
+
+def _cache8_query(q, cache: KvCache8):
+    """(shape, nq) of queries [B, Hq, d] or [B, Hq, nq, d]; checks q against the cache."""
+    if q.dim() not in (3, 4) or q.shape[0] != cache.batch or q.shape[-1] != cache.head_dim:
+        raise ValueError("q must be [B, Hq, d] or [B, Hq, nq, d] with the cache's B and d")
+    return cache.shape(q.shape[1]), (q.shape[2] if q.dim() == 4 else 1)
+
+
+def cache8_attn_workspace(q, cache: KvCache8, *, weights: bool = False) -> int:
+    """Bytes of workspace cache8_attn needs for queries like q."""
+    shape, nq = _cache8_query(q, cache)
+    n = int(load().sfa_cache8_attn_workspace(ctypes.byref(shape), nq, 1 if weights else 0))
+    if n == 0:
+        raise SfaError(4, "sfa_cache8_attn_workspace")
+    return n
+
+
+def cache8_attn(q, cache: KvCache8, *, back: int = 0, scale: float = 0.0, o=None, lse=None, weight_in=None,
+                weight_out=None, workspace=None, status=None, stream=None):
+    """sfa_cache8_attn: attention of q [B, Hq, d] or [B, Hq, nq, d] (the newest nq tokens) over the whole
+    cache; returns o.  With ``weight_out`` every token's attention weight is added to ``weight_in``."""
+    lib = load()
+    shape, nq = _cache8_query(q, cache)
+    dev = cache.k.device
+    _expect(q, "q", q.shape, torch.bfloat16, dev)
+    o = torch.empty_like(q) if o is None else o
+    _expect(o, "o", q.shape, torch.bfloat16, dev)
+    _expect(lse, "lse", q.shape[:-1], torch.float32, dev)
+    tokens = (cache.batch, cache.heads_kv, cache.capacity)
+    _expect(weight_in, "weight_in", tokens, torch.float32, dev)
+    _expect(weight_out, "weight_out", tokens, torch.float32, dev)
+    if workspace is None:
+        workspace = torch.empty(cache8_attn_workspace(q, cache, weights=weight_out is not None), dtype=torch.uint8,
+                                device=dev)
+    _workspace(workspace)
+    _status(status)
+    _check(lib.sfa_cache8_attn(ctypes.byref(shape), ctypes.byref(cache._c), _ptr(q), nq, int(back), float(scale),
+                               _ptr(o), _ptr(lse), _ptr(weight_in), _ptr(weight_out), _ptr(workspace),
+                               workspace.numel(), _ptr(status), _stream(stream)), "sfa_cache8_attn")
+    return o
+
+
+def cache8_attn_list(q, cache: KvCache8, idx, *, scale: float = 0.0, o=None, lse=None, status=None, stream=None):
+    """sfa_cache8_attn_list: attention of q [B, Hq, d] over the tokens of idx [B, Hq, k]; returns o."""
+    lib = load()
+    if q.dim() != 3 or idx.dim() != 3:
+        raise ValueError("q must be [B, Hq, d] and idx [B, Hq, k]")
+    shape, _ = _cache8_query(q, cache)
+    dev = cache.k.device
+    _expect(q, "q", q.shape, torch.bfloat16, dev)
+    o = torch.empty_like(q) if o is None else o
+    _expect(o, "o", q.shape, torch.bfloat16, dev)
+    _expect(idx, "idx", (*q.shape[:2], idx.shape[-1]), torch.int32, dev)
+    _expect(lse, "lse", q.shape[:2], torch.float32, dev)
+    _status(status)
+    _check(lib.sfa_cache8_attn_list(ctypes.byref(shape), ctypes.byref(cache._c), _ptr(q), _ptr(idx), idx.shape[-1],
+                                    float(scale), _ptr(o), _ptr(lse), _ptr(status), _stream(stream)),
+           "sfa_cache8_attn_list")
+    return o
+
+
+def cache8_evict_workspace(src: KvCache8, keep: int) -> int:
+    """Bytes of workspace cache8_evict needs."""
+    n = int(load().sfa_cache8_evict_workspace(ctypes.byref(src.shape(src.heads_kv)), int(keep)))
+    if n == 0:
+        raise SfaError(1, "sfa_cache8_evict_workspace")
+    return n
+
+
+def cache8_evict(src: KvCache8, dst: KvCache8, *, keep: int, recent: int = 0, idx=None, workspace=None, status=None,
+                 stream=None):
+    """sfa_cache8_evict: the last ``recent`` tokens and those of the largest ``src.weight``, ``keep`` in all,
+    move to ``dst``; returns idx [B, Hkv, keep] int32, their rows in src (ascending, -1 padded)."""
+    lib = load()
+    dev = src.k.device
+    if (dst.batch, dst.heads_kv, dst.head_dim) != (src.batch, src.heads_kv, src.head_dim):
+        raise ValueError("dst must have the batch, heads and head dim of src")
+    if dst.k.device != dev:
+        raise ValueError(f"dst must be on {dev}, got {dst.k.device}")
+    if idx is None:
+        idx = torch.empty((src.batch, src.heads_kv, max(int(keep), 0)), dtype=torch.int32, device=dev)
+    _expect(idx, "idx", (src.batch, src.heads_kv, keep), torch.int32, dev)
+    if workspace is not None:
+        _workspace(workspace)
+    _status(status)
+    _check(lib.sfa_cache8_evict(ctypes.byref(src.shape(src.heads_kv)), ctypes.byref(src._c), ctypes.byref(dst._c),
+                                dst.capacity, int(keep), int(recent), _ptr(idx), _ptr(workspace),
+                                0 if workspace is None else workspace.numel(), _ptr(status), _stream(stream)),
+           "sfa_cache8_evict")
+    return idx
+
+
+def cache8_fc_gather(cache: KvCache8, fc, *, K_fc=None, pos0: int = 0, npos: int | None = None, stream=None):
+    """sfa_cache8_fc_gather: the compact dominant-pair copy K_fc [B, Hkv, capacity, 2 nfc] bf16 of the cached keys."""
+    lib = load()
+    fch, nfc = _fc_host(fc)
+    rows = (cache.batch, cache.heads_kv, cache.capacity, 2 * nfc)
+    if len(fch) != cache.heads_kv * nfc:
+        raise ValueError("fc must have a row per KV head")
+    K_fc = torch.empty(rows, dtype=torch.bfloat16, device=cache.k.device) if K_fc is None else K_fc
+    _expect(K_fc, "K_fc", rows, torch.bfloat16, cache.k.device)
+    npos = cache.capacity - pos0 if npos is None else npos
+    _check(lib.sfa_cache8_fc_gather(ctypes.byref(cache.shape(cache.heads_kv)), ctypes.byref(cache._c), fch, nfc, pos0,
+                                    npos, _ptr(K_fc), _stream(stream)), "sfa_cache8_fc_gather")
+    return K_fc
 
 
 def selftest_bounded_wait(limit_ms: int, complete: bool, device="cuda", stream=None) -> int:

@@ -10,7 +10,9 @@
  *   2. exact softmax attention over the kept key blocks only (§1);
  * and the decode-side analogue of "FASA: Frequency-aware Sparse Attention"
  * (§2B): token importance of a KV cache from dominant rotary pairs, the top-k
- * tokens, and exact attention of one query token over them (sfa_decode_*).
+ * tokens, and exact attention of one query token over them (sfa_decode_*); and
+ * an 8-bit KV cache for the decode side with the calls that fill, read, weigh
+ * and evict it (sfa_cache8_*).
  *
  * Conventions shared by every entry point:
  *   - Tensors are contiguous, row-major, layout [B, H, L, d] (batch, head,
@@ -339,6 +341,132 @@ sfa_status sfa_decode_select(const sfa_shape* shape, const void* q, const void* 
 sfa_status sfa_decode_attn(const sfa_shape* shape, const void* q, const void* K_cache,
                            const void* V_cache, const int* idx, int k, float scale, void* o,
                            float* lse, int* status_word, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * 8-bit KV cache for the decode side.  Keys and values are held as e4m3 codes
+ * (8 bits: sign, 4 exponent bits, 3 fraction bits, largest value 448) with one
+ * float32 scale per block of `block` tokens and KV head:
+ *   value = code * scale.
+ * Every scale is a power of two, so dividing by it is exact and a code is the
+ * value rounded once:  need(a) = the smallest 2^e, e >= -126, with a <= 448 * 2^e.
+ * A cache of capacity L = shape->seq_len holds, all in caller-owned device memory:
+ *   k, v              [B, heads_kv, L, d] e4m3 codes, 16-byte aligned; keys rotated
+ *                     at their original positions
+ *   k_scale, v_scale  [B, heads_kv, ceil(L / block)] float32
+ *   lens              [B] int32: tokens [0, lens[b]) of sequence b are valid
+ *   weight            [B, heads_kv, L] float32: attention weight each token has
+ *                     received so far (may be NULL where a call does not use it)
+ * Rows at and after lens[b] are never read into a result and may hold anything.
+ * Shape rules: those of the decode calls above (dtype SFA_BF16; d in {64, 128};
+ * heads_q / heads_kv in {1, 2, 4, 8}; batch * heads_kv * L < 2^31), block in
+ * {64, 128} (SFA_ERR_SHAPE); any L >= 1.  A length or position found out of
+ * range on the device sets status_word to SFA_ERR_INDEX.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t* lens;
+  float* weight;
+  int32_t block;
+} sfa_cache8;
+
+/*
+ * Quantise n new rows per sequence into the cache.  K_new, V_new [B, heads_kv, n, d]
+ * bf16 (16-byte aligned); sequence b takes the first counts[b] of them (device
+ * [B] int32, 0 .. n; NULL: all n) at rows [p, p + counts[b]), where p = at[b]
+ * (device [B] int32; NULL: lens[b], an append).  Afterwards lens[b] = p + counts[b].
+ * A block that receives rows gets the scale need(largest |new element|), or the
+ * larger of that and its present scale if it has rows before p; where that
+ * raises the scale, the codes of those earlier rows are rounded to it.  NaN and
+ * infinite elements are stored as NaN and do not count towards the scale.  The
+ * accumulated weight of the new rows becomes 0 (where cache->weight is not
+ * NULL).  A sequence whose position, count or end (> L) is out of range is left
+ * as it was and status_word (device, nullable) set to SFA_ERR_INDEX.  n = 0 is
+ * SFA_ERR_INVALID_ARG.  heads_q of the shape is not used.  at must not overlap
+ * cache->lens (pass NULL for that).  Launches 1 kernel, 2 with at = NULL.
+ */
+sfa_status sfa_cache8_append(const sfa_shape* shape, const sfa_cache8* cache, const void* K_new,
+                             const void* V_new, int n, const int32_t* at, const int32_t* counts,
+                             int* status_word, void* stream);
+
+/*
+ * Bytes of workspace sfa_cache8_attn needs (0 if the arguments are invalid);
+ * weights != 0 for calls with weight_out.
+ */
+size_t sfa_cache8_attn_workspace(const sfa_shape* shape, int nq, int weights);
+
+/*
+ * Attention of the newest query tokens over the whole cache.  q [B, heads_q, nq, d]
+ * bf16 holds the last nq of the visible n_b = max(lens[b] - back, 0) tokens'
+ * queries, already rotated: query i sees tokens t < n_b - (nq - 1 - i).
+ *   o_i = sum_t softmax_t(scale * q_i . k_t) v_t,  lse_i = log sum_t exp(scale * q_i . k_t)
+ * o [B, heads_q, nq, d] bf16; lse [B, heads_q, nq] float32 (nullable, natural
+ * log).  A query that sees nothing gives o = 0 and lse = -inf.  scale <= 0
+ * selects 1/sqrt(d).  nq >= 1 and nq * heads_q / heads_kv <= 16
+ * (SFA_ERR_UNSUPPORTED).  back >= 0 ignores the newest `back` tokens (earlier
+ * queries of a prompt, seen after it has been stored).
+ * With weight_out (nullable, [B, heads_kv, L] float32), for every t < n_b:
+ *   weight_out_t = weight_in_t + sum over the group's heads and the nq queries
+ *   of exp(scale * q_i . k_t - lse_i)   (the queries that see t)
+ * weight_in like weight_out, NULL = 0; the two may be the same array
+ * (cache->weight itself to accumulate; that pointer is not used by this call).
+ * Other elements of weight_out are left alone.  The sums have a fixed order:
+ * the same call gives the same bits.
+ * A q element that is NaN or infinite makes its row's o NaN.
+ * workspace: device, at least sfa_cache8_attn_workspace() bytes, 256-byte
+ * aligned; nothing in it is kept between calls, and calls whose kernels overlap
+ * on the GPU need one each.  A length outside [0, L] counts as 0.
+ */
+sfa_status sfa_cache8_attn(const sfa_shape* shape, const sfa_cache8* cache, const void* q, int nq,
+                           int back, float scale, void* o, float* lse, const float* weight_in,
+                           float* weight_out, void* workspace, size_t workspace_bytes,
+                           int* status_word, void* stream);
+
+/*
+ * sfa_decode_attn over the 8-bit cache: one query token q [B, heads_q, d] over
+ * the tokens listed in idx [B, heads_q, k] (-1 entries skipped, any order).  An
+ * entry outside [-1, lens[b]) sets status_word to SFA_ERR_INDEX and that row's
+ * o = 0, lse = -inf; an empty row likewise.  Other arguments as sfa_decode_attn.
+ */
+sfa_status sfa_cache8_attn_list(const sfa_shape* shape, const sfa_cache8* cache, const void* q,
+                                const int* idx, int k, float scale, void* o, float* lse,
+                                int* status_word, void* stream);
+
+/* Bytes of workspace sfa_cache8_evict needs where idx is NULL (0 if invalid). */
+size_t sfa_cache8_evict_workspace(const sfa_shape* shape, int keep);
+
+/*
+ * Eviction by accumulated attention weight.  For each (b, KV head) with n = lens[b]:
+ * all tokens if n <= keep, else the last `recent` ones and, of the others, the
+ * keep - recent with the largest weight (weight desc, index asc; NaN above
+ * everything, -0 = +0).  The kept tokens move in order to rows [0, min(n, keep))
+ * of dst (a cache of capacity dst_len >= keep, same block), every dst block
+ * quantised afresh from its tokens' values by sfa_cache8_append's rule: codes
+ * keep their value unless a common scale pushes them below e4m3's normal range.
+ * NaN codes stay NaN.  weight moves along (where both caches have it; src's is
+ * required), dst lens[b] = min(n, keep).  dst rows, scales and weights behind
+ * the kept ones are left as they were.  idx [B, heads_kv, keep] int32
+ * (nullable): the kept tokens' src rows ascending, padded with -1.
+ * 1 <= keep, 0 <= recent <= keep.  dst's arrays must not overlap src's
+ * (SFA_ERR_INVALID_ARG).  A bad length counts as 0 and sets status_word.
+ * workspace (256-byte aligned) is used only where idx is NULL.
+ */
+sfa_status sfa_cache8_evict(const sfa_shape* shape, const sfa_cache8* src, const sfa_cache8* dst,
+                            int dst_len, int keep, int recent, int* idx, void* workspace,
+                            size_t workspace_bytes, int* status_word, void* stream);
+
+/*
+ * sfa_decode_fc_gather from the 8-bit cache: K_fc [B, heads_kv, L, 2 nfc] bf16
+ * rows [pos0, pos0 + npos) from the cached keys' values (exact in bf16, so a
+ * selection on K_fc ranks the keys that the attention reads).  Rows are copied
+ * whether or not they lie below lens[b].  fc, nfc, errors as sfa_decode_fc_gather.
+ */
+sfa_status sfa_cache8_fc_gather(const sfa_shape* shape, const sfa_cache8* cache, const int* fc,
+                                int nfc, int pos0, int npos, void* K_fc, void* stream);
 
 /*
  * Diagnostics (no counterpart in the pages): exercises the bounded wait that
