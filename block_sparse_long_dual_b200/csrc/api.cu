@@ -512,6 +512,19 @@ Cache8Ws cache8_ws(const sfa_shape* s, int cols, bool weights) {
   return w;
 }
 
+// The codes as a 2-D tensor [rows, d] of bytes, boxes of 128 rows, swizzled over a row's width.
+bool make_code_map(CUtensorMap* m, const void* base, uint64_t rows, int d) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)d, rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)d};
+  const cuuint32_t box[2] = {(cuuint32_t)d, (cuuint32_t)c8::kTile};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   if (a == nullptr || b == nullptr) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -587,7 +600,10 @@ sfa_status sfa_cache8_attn(const sfa_shape* shape, const sfa_cache8* cache, cons
   p.scores = weight_out != nullptr ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
   p.nq = nq; p.cols = cols; p.back = back; p.G = cache8_ctas(shape); p.Lp = cache8_row(shape);
   p.sl2 = (scale > 0.f ? scale : (float)(1.0 / sqrt((double)shape->head_dim))) * 1.4426950408889634f;
-  return cuda_status(launch_cache8_attn(p, as_stream(stream)));
+  CUtensorMap tk, tv;
+  const uint64_t rows = (uint64_t)p.B * p.Hkv * p.L;
+  if (!make_code_map(&tk, cache->k, rows, p.D) || !make_code_map(&tv, cache->v, rows, p.D)) return SFA_ERR_CUDA;
+  return cuda_status(launch_cache8_attn(p, tk, tv, as_stream(stream)));
 }
 
 sfa_status sfa_cache8_attn_list(const sfa_shape* shape, const sfa_cache8* cache, const void* q, const int* idx, int k,

@@ -2,6 +2,7 @@
 // is split over CTAs.  Shared by cache8_store.cu and cache8_attn.cu.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -198,7 +199,9 @@ struct Cache8Gather {
 cudaError_t launch_cache8_append(const Cache8Append& p, cudaStream_t st);
 cudaError_t launch_cache8_evict(const Cache8Evict& p, cudaStream_t st);
 cudaError_t launch_cache8_gather(const Cache8Gather& p, cudaStream_t st);
-cudaError_t launch_cache8_attn(const Cache8Attn& p, cudaStream_t st);
+// tk, tv: the code arrays as 2-D tensors of D-byte rows, boxes of D x 128, swizzle as wide as a row.
+cudaError_t launch_cache8_tiles(const Cache8Attn& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st);
+cudaError_t launch_cache8_attn(const Cache8Attn& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st);
 cudaError_t launch_cache8_attn_list(const Cache8Attn& p, cudaStream_t st);
 
 }  // namespace sfa

@@ -1,9 +1,8 @@
-// Attention over the 8-bit KV cache: the whole cache (split over CTAs, then
-// joined), the accumulated weights, and index lists.
+// Attention over the 8-bit KV cache: joining the pieces of the whole-cache attention
+// (cache8_attn_tc.cu), the accumulated weights, and index lists.
 #include <math.h>
 
 #include "cache8.cuh"
-#include "tc_ptx.cuh"
 
 namespace sfa {
 
@@ -12,132 +11,6 @@ namespace {
 using namespace c8;
 
 constexpr float kLn2 = 0.6931471805599453f;
-
-// ---------------------------------------------------------------------------
-// Whole cache, one piece per (CTA, unit): CUDA-core version.  A tile's scores
-// are taken with a thread per token, its values summed with a thread per dim.
-// ---------------------------------------------------------------------------
-template <int D, int NC>
-__global__ void __launch_bounds__(kTile) attn_split_kernel(Cache8Attn p) {
-  __shared__ float sq[NC][D];
-  __shared__ float se[NC][kTile];
-  __shared__ float sred[NC][4];
-  __shared__ float svs[kTile];
-  __shared__ long long sh_total, sh_before;
-  __shared__ int sh_b;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (warp == 0) {
-    long long dummy, before = 0;
-    const long long total = warp_count_tiles(p.lens, p.B, p.Hkv, p.L, p.back, 0, &dummy, p.status);
-    const Split s(total, p.G);
-    const long long x0 = s.start(blockIdx.x);
-    int b = -1;
-    if (x0 < s.start(blockIdx.x + 1)) b = warp_find_seq(p.lens, p.B, p.Hkv, p.L, p.back, x0, &before);
-    if (lane == 0) { sh_total = total; sh_before = before; sh_b = b; }
-  }
-  __syncthreads();
-  const Split split(sh_total, p.G);
-  long long x = split.start(blockIdx.x);
-  const long long x1 = split.start(blockIdx.x + 1);
-  int b = sh_b;
-  long long before = sh_before;  // tiles before sequence b
-  while (x < x1) {
-    const int nv = visible(p.lens, b, p.L, p.back, nullptr);
-    const int tiles = (nv + kTile - 1) / kTile;
-    if (x >= before + (long long)tiles * p.Hkv) { before += (long long)tiles * p.Hkv; ++b; continue; }
-    const int g = (int)((x - before) / tiles);
-    int tile = (int)((x - before) % tiles);
-    const int last = (int)min((long long)tiles, tile + (x1 - x));  // this piece: tiles [tile, last)
-    const int unit = b * p.Hkv + g;
-    __syncthreads();
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (size_t)unit * p.cols * D;
-    for (int i = tid; i < NC * D; i += kTile) sq[i / D][i % D] = i < p.cols * D ? __bfloat162float(q[i]) : 0.f;
-    float m[NC], l[NC], acc[NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) { m[c] = -INFINITY; l[c] = 0.f; acc[c] = 0.f; }
-    x += last - tile;
-    for (; tile < last; ++tile) {
-      const int t = tile * kTile + tid;
-      float s[NC];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) s[c] = 0.f;
-      __syncthreads();
-      svs[tid] = t < nv ? p.vs[(size_t)unit * p.nblk + t / p.T] : 0.f;
-      if (t < nv) {
-        const uint4* kr = reinterpret_cast<const uint4*>(p.k + ((size_t)unit * p.L + t) * D);
-        for (int i = 0; i < D / 16; ++i) {
-          const uint4 u = __ldg(kr + i);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float kv[4];
-            from_e4m3x4(w[e], kv);
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-              for (int z = 0; z < 4; ++z) s[c] = fmaf(sq[c][i * 16 + e * 4 + z], kv[z], s[c]);
-          }
-        }
-      }
-      const float f = t < nv ? p.ks[(size_t)unit * p.nblk + t / p.T] * p.sl2 : 0.f;
-      float mt[NC];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const bool sees = c < p.cols && t < nv - (p.nq - 1 - c % p.nq);
-        s[c] = sees ? s[c] * f : -INFINITY;
-        float v = s[c];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-        if (lane == 0) sred[c][warp] = v;
-        if (p.w_out != nullptr && c < p.cols && t < nv) p.scores[((size_t)unit * p.cols + c) * p.Lp + t] = s[c];
-      }
-      __syncthreads();
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        mt[c] = fmaxf(fmaxf(sred[c][0], sred[c][1]), fmaxf(sred[c][2], sred[c][3]));
-        const float mn = fmaxf(m[c], mt[c]);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float keep = exp2f(m[c] - base);
-        const float e = exp2f(s[c] - base);
-        l[c] = l[c] * keep + e;
-        acc[c] *= keep;
-        m[c] = mn;
-        se[c][tid] = s[c] == -INFINITY ? 0.f : e;
-      }
-      __syncthreads();
-      if (tid < D) {
-        const int rows = min(kTile, nv - tile * kTile);
-        const uint8_t* vr = p.v + ((size_t)unit * p.L + (size_t)tile * kTile) * D + tid;
-        for (int r = 0; r < rows; ++r) {
-          const float v = __low2float(from_e4m3x2(vr[(size_t)r * D])) * svs[r];
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const float e = se[c][r];
-            if (e != 0.f) acc[c] = fmaf(e, v, acc[c]);
-          }
-        }
-      }
-    }
-    const size_t slot = (size_t)blockIdx.x + unit;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      float v = l[c];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      __syncthreads();
-      if (lane == 0) sred[c][warp] = v;
-      __syncthreads();
-      if (c < p.cols) {
-        if (tid == 0) {
-          float* ml = p.part_ml + (slot * p.cols + c) * 2;
-          ml[0] = m[c];
-          ml[1] = sred[c][0] + sred[c][1] + sred[c][2] + sred[c][3];
-        }
-        if (tid < D) p.part_o[(slot * p.cols + c) * D + tid] = acc[c];
-      }
-    }
-  }
-}
 
 // Joins the pieces of one (unit, query row): CTA per (row, unit), a thread per dim.
 template <int D>
@@ -309,15 +182,8 @@ __global__ void __launch_bounds__(WARPS * 32) attn_list_kernel(Cache8Attn p) {
 
 }  // namespace
 
-cudaError_t launch_cache8_attn(const Cache8Attn& p, cudaStream_t st) {
-  if (p.D == 128) {
-    if (p.cols <= 8) attn_split_kernel<128, 8><<<p.G, kTile, 0, st>>>(p);
-    else attn_split_kernel<128, 16><<<p.G, kTile, 0, st>>>(p);
-  } else {
-    if (p.cols <= 8) attn_split_kernel<64, 8><<<p.G, kTile, 0, st>>>(p);
-    else attn_split_kernel<64, 16><<<p.G, kTile, 0, st>>>(p);
-  }
-  cudaError_t e = cudaGetLastError();
+cudaError_t launch_cache8_attn(const Cache8Attn& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
+  cudaError_t e = launch_cache8_tiles(p, tk, tv, st);
   if (e != cudaSuccess) return e;
   const unsigned rows = (unsigned)(p.B * p.Hkv * p.cols);
   if (p.D == 128) attn_join_kernel<128><<<rows, 128, 0, st>>>(p);
