@@ -482,14 +482,17 @@ sfa_status check_cache8_arrays(const sfa_cache8* c) {
 }
 
 struct Cache8Ws {
-  size_t ml, o, lse2, scores, total;
+  size_t ml, o, scores, total;
 };
 
 // Pieces of the split attention: one per CTA and unit cut at most (cache8.cuh).
-int cache8_ctas(const sfa_shape* s) {
-  const long long tiles = (long long)s->batch * s->heads_kv * ((s->seq_len + c8::kTile - 1) / c8::kTile);
-  return (int)(tiles < c8::kMaxCtas ? tiles : c8::kMaxCtas);
+int cache8_ctas(const sfa_shape* s, int cols) {
+  const int tile = c8::tile_tokens(s->head_dim, cols);
+  const long long tiles = (long long)s->batch * s->heads_kv * ((s->seq_len + tile - 1) / tile);
+  return (int)(tiles < c8::kSms * c8::kCtasPerSm ? tiles : c8::kSms * c8::kCtasPerSm);
 }
+
+int cache8_cpad(int cols) { return cols <= 2 ? cols : (cols + 3) / 4 * 4; }
 
 int cache8_row(const sfa_shape* s) { return (s->seq_len + 127) / 128 * 128; }
 
@@ -502,23 +505,22 @@ sfa_status cache8_cols(const sfa_shape* s, int nq, int* cols) {
 }
 
 Cache8Ws cache8_ws(const sfa_shape* s, int cols, bool weights) {
-  const size_t units = (size_t)s->batch * s->heads_kv, slots = units + cache8_ctas(s);
+  const size_t units = (size_t)s->batch * s->heads_kv, slots = units + cache8_ctas(s, cols);
   Cache8Ws w;
   w.ml = 0;
   w.o = align256(w.ml + slots * cols * 2 * sizeof(float));
-  w.lse2 = align256(w.o + slots * cols * s->head_dim * sizeof(float));
-  w.scores = align256(w.lse2 + units * cols * sizeof(float));
-  w.total = align256(w.scores + (weights ? units * cols * (size_t)cache8_row(s) * sizeof(float) : 0));
+  w.scores = align256(w.o + slots * cols * s->head_dim * sizeof(float));
+  w.total = align256(w.scores + (weights ? units * cache8_cpad(cols) * (size_t)cache8_row(s) * sizeof(float) : 0));
   return w;
 }
 
-// The codes as a 2-D tensor [rows, d] of bytes, boxes of 128 rows, swizzled over a row's width.
-bool make_code_map(CUtensorMap* m, const void* base, uint64_t rows, int d) {
+// The codes as a 2-D tensor [rows, d] of bytes, boxes of `tile` rows, swizzled over a row's width.
+bool make_code_map(CUtensorMap* m, const void* base, uint64_t rows, int d, int tile) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)d, rows};
   const cuuint64_t strides[1] = {(cuuint64_t)d};
-  const cuuint32_t box[2] = {(cuuint32_t)d, (cuuint32_t)c8::kTile};
+  const cuuint32_t box[2] = {(cuuint32_t)d, (cuuint32_t)tile};
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -596,13 +598,12 @@ sfa_status sfa_cache8_attn(const sfa_shape* shape, const sfa_cache8* cache, cons
   p.q = q; p.o = o; p.lse = lse; p.w_in = weight_in; p.w_out = weight_out; p.status = status_word;
   p.part_ml = reinterpret_cast<float*>(ws + w.ml);
   p.part_o = reinterpret_cast<float*>(ws + w.o);
-  p.lse2 = reinterpret_cast<float*>(ws + w.lse2);
   p.scores = weight_out != nullptr ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
-  p.nq = nq; p.cols = cols; p.back = back; p.G = cache8_ctas(shape); p.Lp = cache8_row(shape);
+  p.nq = nq; p.cols = cols; p.cpad = cache8_cpad(cols); p.back = back; p.tile = c8::tile_tokens(p.D, cols); p.G = cache8_ctas(shape, cols); p.Lp = cache8_row(shape);
   p.sl2 = (scale > 0.f ? scale : (float)(1.0 / sqrt((double)shape->head_dim))) * 1.4426950408889634f;
   CUtensorMap tk, tv;
   const uint64_t rows = (uint64_t)p.B * p.Hkv * p.L;
-  if (!make_code_map(&tk, cache->k, rows, p.D) || !make_code_map(&tv, cache->v, rows, p.D)) return SFA_ERR_CUDA;
+  if (!make_code_map(&tk, cache->k, rows, p.D, p.tile) || !make_code_map(&tv, cache->v, rows, p.D, p.tile)) return SFA_ERR_CUDA;
   return cuda_status(launch_cache8_attn(p, tk, tv, as_stream(stream)));
 }
 

@@ -51,24 +51,33 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 // ---------------------------------------------------------------------------
-// Work split of the whole-cache attention.  The tiles (kTile tokens of one
-// (b, KV head)) of all sequences form one list, ordered (b, head, tile); CTA i
-// of the G working ones takes tiles [i T / G, (i + 1) T / G): equal shares whatever the lengths.
-// A share that crosses a head's end is cut there; the piece of unit u = b Hkv + g
-// in CTA i has the partial-result slot i + u (both only grow along the list, and
-// one grows at every cut, so no two pieces share a slot).
+// Work split of the whole-cache attention.  The tiles (`tile` tokens of one
+// (b, KV head)) of all sequences form one list, ordered (b, head, tile); the G
+// working CTAs take consecutive shares of it, equal to within one tile whatever
+// the lengths.  A share that crosses a head's end is cut there; the piece of
+// unit u = b Hkv + g in CTA i has the partial-result slot i + u (both only grow
+// along the list, and one grows at every cut, so no two pieces share a slot).
+// All tiles together are fewer than 2^31 (B Hkv L is), so the list is indexed in
+// 32 bits.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 128;
-constexpr int kMaxCtas = 2 * 148;  // two per SM
-constexpr int kMaxCols = 16;       // query rows (heads of the group x query tokens) of a unit
+constexpr int kSms = 148, kCtasPerSm = 2;
+constexpr int kMaxCols = 16;  // query rows (heads of the group x query tokens) of a unit
+
+// Tokens of a tile: a softmax thread holds one token's row of scores, and two where the row is short
+// and the token's bytes are few (cache8_attn_tc.cu).
+__host__ __device__ constexpr int tile_tokens(int D, int cols) { return D == 64 && cols <= 8 ? 256 : 128; }
 
 struct Split {
-  long long total;  // tiles of all units
-  int G;            // CTAs with a share: as many as launched, or one per tile where there are fewer
-                    // tiles, so that no share between two others is empty
-  __device__ Split(long long t, int launched) : total(t), G(t < launched ? (int)t : launched) {}
-  __device__ long long start(int i) const { return i < G ? total * i / G : total; }
-  __device__ int owner(long long t) const { return (int)(((t + 1) * G + total - 1) / total) - 1; }
+  int total;  // tiles of all units
+  int G;      // CTAs with a share: as many as launched, or one per tile where there are fewer tiles,
+              // so that no share between two others is empty
+  int q, r;   // the first r CTAs take q + 1 tiles, the others q
+  __device__ Split(int t, int launched) : total(t), G(t < launched ? t : launched) {
+    q = G > 0 ? total / G : 0;
+    r = G > 0 ? total % G : 0;
+  }
+  __device__ int start(int i) const { return i < G ? i * q + min(i, r) : total; }
+  __device__ int owner(int t) const { return t < r * (q + 1) ? t / (q + 1) : r + (t - r * (q + 1)) / q; }
 };
 
 __device__ __forceinline__ int visible(const int* lens, int b, int L, int back, int* status) {
@@ -80,49 +89,61 @@ __device__ __forceinline__ int visible(const int* lens, int b, int L, int back, 
   return n > back ? n - back : 0;
 }
 
-// One warp: total tiles of the batch (all heads), and the tiles before sequence b_at.
-__device__ __forceinline__ long long warp_count_tiles(const int* lens, int B, int Hkv, int L, int back, int b_at,
-                                                      long long* before, int* status) {
-  const int lane = threadIdx.x & 31;
-  long long all = 0, pre = 0;
-  for (int b = lane; b < B; b += 32) {
-    const long long t = (long long)((visible(lens, b, L, back, status) + kTile - 1) / kTile) * Hkv;
-    all += t;
-    if (b < b_at) pre += t;
-  }
+// One warp, all lanes: the tiles of 32 sequences from b0 on, as an inclusive sum per lane.
+__device__ __forceinline__ int warp_scan_tiles(const int* lens, int b0, int B, int Hkv, int L, int back, int tile,
+                                               int* mine, int* status) {
+  const int lane = threadIdx.x & 31, b = b0 + lane;
+  *mine = b < B ? (visible(lens, b, L, back, status) + tile - 1) / tile * Hkv : 0;
+  int inc = *mine;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    pre += __shfl_xor_sync(0xffffffffu, pre, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  return inc;
+}
+
+// One warp: tiles of the whole batch, and of the sequences before b_at.
+__device__ __forceinline__ int warp_count_tiles(const int* lens, int B, int Hkv, int L, int back, int tile, int b_at,
+                                                int* before) {
+  int all = 0, pre = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    int mine;
+    const int inc = warp_scan_tiles(lens, b0, B, Hkv, L, back, tile, &mine, nullptr);
+    if (b_at >= b0 && b_at < b0 + 32) pre = all + __shfl_sync(0xffffffffu, inc - mine, b_at - b0);
+    all += __shfl_sync(0xffffffffu, inc, 31);
   }
   *before = pre;
   return all;
 }
 
-// One warp: the sequence that tile x of the list belongs to, and the tiles before it (x < total).
-__device__ __forceinline__ int warp_find_seq(const int* lens, int B, int Hkv, int L, int back, long long x,
-                                             long long* before) {
-  const int lane = threadIdx.x & 31;
-  long long base = 0;
+// One warp: the share of CTA i of `launched`: its tiles (0: none), its first sequence, and that sequence's tiles
+// before the share.
+__device__ __forceinline__ int warp_share(const int* lens, int B, int Hkv, int L, int back, int tile, int launched,
+                                          int i, int* b_first, int* skip, int* status) {
+  int mine, inc = warp_scan_tiles(lens, 0, B, Hkv, L, back, tile, &mine, status);
+  int total = __shfl_sync(0xffffffffu, inc, 31);
+  for (int b0 = 32; b0 < B; b0 += 32) {
+    int m2;
+    total += __shfl_sync(0xffffffffu, warp_scan_tiles(lens, b0, B, Hkv, L, back, tile, &m2, status), 31);
+  }
+  const Split s(total, launched);
+  const int x0 = s.start(i), n = s.start(i + 1) - x0;
+  *b_first = *skip = 0;
+  if (n <= 0) return 0;
+  int base = 0;
   for (int b0 = 0; b0 < B; b0 += 32) {
-    const int b = b0 + lane;
-    const long long t = b < B ? (long long)((visible(lens, b, L, back, nullptr) + kTile - 1) / kTile) * Hkv : 0;
-    long long inc = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += u;
-    }
-    const unsigned in = __ballot_sync(0xffffffffu, x < base + inc);
+    if (b0 > 0) inc = warp_scan_tiles(lens, b0, B, Hkv, L, back, tile, &mine, nullptr);
+    const unsigned in = __ballot_sync(0xffffffffu, x0 < base + inc);
     if (in != 0) {
       const int l = __ffs(in) - 1;
-      *before = base + __shfl_sync(0xffffffffu, inc - t, l);
-      return b0 + l;
+      *b_first = b0 + l;
+      *skip = x0 - base - __shfl_sync(0xffffffffu, inc - mine, l);
+      return n;
     }
     base += __shfl_sync(0xffffffffu, inc, 31);
   }
-  *before = 0;
-  return -1;
+  return 0;  // only if the lengths changed under the call
 }
 
 }  // namespace c8
@@ -161,12 +182,11 @@ struct Cache8Attn {
   // workspace
   float* part_ml;     // [G + U, cols, 2] running maximum (log2 units) and sum of each piece
   float* part_o;      // [G + U, cols, D]
-  float* lse2;        // [U, cols] log2 of the sum of 2^score
-  float* scores;      // [U, cols, Lp] log2-unit scores (only with w_out)
+  float* scores;      // [U, Lp, cpad] log2-unit scores (only with w_out); cpad: cols rounded up to 1, 2 or 4 n
   // list attention
   const int* idx;
   int k_list;
-  int B, Hq, Hkv, L, D, T, nblk, nq, cols, back, G, Lp;
+  int B, Hq, Hkv, L, D, T, nblk, nq, cols, cpad, back, tile, G, Lp;
   float sl2;          // softmax scale * log2(e)
 };
 
@@ -199,7 +219,7 @@ struct Cache8Gather {
 cudaError_t launch_cache8_append(const Cache8Append& p, cudaStream_t st);
 cudaError_t launch_cache8_evict(const Cache8Evict& p, cudaStream_t st);
 cudaError_t launch_cache8_gather(const Cache8Gather& p, cudaStream_t st);
-// tk, tv: the code arrays as 2-D tensors of D-byte rows, boxes of D x 128, swizzle as wide as a row.
+// tk, tv: the code arrays as 2-D tensors of D-byte rows, boxes of D x tile, swizzle as wide as a row.
 cudaError_t launch_cache8_tiles(const Cache8Attn& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st);
 cudaError_t launch_cache8_attn(const Cache8Attn& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st);
 cudaError_t launch_cache8_attn_list(const Cache8Attn& p, cudaStream_t st);

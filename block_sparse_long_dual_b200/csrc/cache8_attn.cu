@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include "cache8.cuh"
+#include "tc_ptx.cuh"
 
 namespace sfa {
 
@@ -12,57 +13,187 @@ using namespace c8;
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Joins the pieces of one (unit, query row): CTA per (row, unit), a thread per dim.
-template <int D>
-__global__ void __launch_bounds__(D) attn_join_kernel(Cache8Attn p) {
-  __shared__ long long sh_total, sh_t0;
-  const int unit = blockIdx.x / p.cols, c = blockIdx.x % p.cols, b = unit / p.Hkv, g = unit % p.Hkv;
+// ---------------------------------------------------------------------------
+// Joining the pieces.  The first B Hkv cols CTAs each join one query row of one
+// unit (a thread per dim, the row's pieces shared among the thread groups); the
+// others, with weights, each add the attention weights of some chunks of tokens
+// of one unit: the rows' log-sum-exps again from the pieces' maxima and sums (a few
+// numbers), then exp2 of the scores that the first step left, summed over the
+// rows in order.  Launched while the first step still runs: everything up to
+// pieces_ready() needs only the lengths.
+// ---------------------------------------------------------------------------
+constexpr int kJoinThreads = 256;
+
+__device__ __forceinline__ void pieces_ready() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Tokens per thread of the weights part: about eight 16-byte loads of scores in flight.
+constexpr int weight_tokens(int CP) { return CP <= 4 ? 8 : (CP == 8 ? 4 : 2); }
+
+template <int D, int CP>  // CP = p.cpad
+__global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid_constant__ Cache8Attn p, int parts,
+                                                                   int per_part) {
+  constexpr int GR = kJoinThreads / D;  // thread groups
+  constexpr int TPT = weight_tokens(CP);
+  __shared__ int sh_total, sh_t0;
+  __shared__ float so[GR][D], sl[GR];
+  __shared__ __align__(16) float slse[kMaxCols];
   const int tid = threadIdx.x;
+  const unsigned rows = (unsigned)(p.B * p.Hkv * p.cols);
+  const bool join = blockIdx.x < rows;
+  const int unit = join ? blockIdx.x / p.cols : (blockIdx.x - rows) / parts;
+  const int b = unit / p.Hkv, g = unit % p.Hkv;
   const int nv = visible(p.lens, b, p.L, p.back, nullptr);
-  const int tiles = (nv + kTile - 1) / kTile;
+  const int tiles = (nv + p.tile - 1) / p.tile;
+  constexpr int CHUNK = TPT * kJoinThreads;
+  const int part0 = join ? 0 : (int)((blockIdx.x - rows) % parts) * per_part;  // this CTA's tokens
+  if (!join && part0 >= nv) return;
   if (tid < 32) {
-    long long before;
-    const long long total = warp_count_tiles(p.lens, p.B, p.Hkv, p.L, p.back, b, &before, nullptr);
-    if (tid == 0) { sh_total = total; sh_t0 = before + (long long)g * tiles; }
+    int before;
+    const int total = warp_count_tiles(p.lens, p.B, p.Hkv, p.L, p.back, p.tile, b, &before);
+    if (tid == 0) { sh_total = total; sh_t0 = before + g * tiles; }
   }
   __syncthreads();
-  float M = -INFINITY, L = 0.f, o = 0.f;
+  size_t s0 = 0;  // the unit's pieces have the slots [s0, s0 + np)
+  int np = 0;
   if (tiles > 0) {
     const Split s(sh_total, p.G);
-    const int i0 = s.owner(sh_t0), i1 = s.owner(sh_t0 + tiles - 1);
-    for (int i = i0; i <= i1; ++i) M = fmaxf(M, p.part_ml[(((size_t)i + unit) * p.cols + c) * 2]);
-    const float base = M == -INFINITY ? 0.f : M;
-    for (int i = i0; i <= i1; ++i) {
-      const size_t slot = ((size_t)i + unit) * p.cols + c;
-      const float f = exp2f(p.part_ml[slot * 2] - base);
-      L += p.part_ml[slot * 2 + 1] * f;
-      o = fmaf(p.part_o[slot * D + tid], f, o);
-    }
+    const int i0 = s.owner(sh_t0);
+    np = s.owner(sh_t0 + tiles - 1) - i0 + 1;
+    s0 = (size_t)i0 + unit;
   }
-  // L = 0 exactly when the row sees no token (a NaN score makes L NaN, and the row's o)
-  const size_t row = (size_t)unit * p.cols + c;
-  static_cast<__nv_bfloat16*>(p.o)[row * D + tid] = __float2bfloat16_rn(L == 0.f ? 0.f : o / L);
-  if (tid == 0) {
-    const float l2 = L == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) + log2f(L);
-    if (p.lse != nullptr) p.lse[row] = l2 * kLn2;
-    if (p.w_out != nullptr) p.lse2[row] = l2;
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  pieces_ready();
+  if (join) {
+    const int c = blockIdx.x % p.cols, grp = tid / D, r = tid % D;
+    float M = -INFINITY;
+    for (int i = 0; i < np; ++i) M = fmaxf(M, ml[(s0 + i) * p.cols + c].x);
+    const float base = M == -INFINITY ? 0.f : M;
+    float l = 0.f, o = 0.f;
+#pragma unroll 4
+    for (int i = grp; i < np; i += GR) {
+      const size_t at = (s0 + i) * p.cols + c;
+      const float2 x = ml[at];
+      const float f = exp2f(x.x - base);
+      l = fmaf(x.y, f, l);
+      o = fmaf(p.part_o[at * D + r], f, o);
+    }
+    so[grp][r] = o;
+    if (r == 0) sl[grp] = l;
+    __syncthreads();
+    if (tid >= D) return;
+    l = sl[0];
+    o = so[0][tid];
+#pragma unroll
+    for (int i = 1; i < GR; ++i) {
+      l += sl[i];
+      o += so[i][tid];
+    }
+    // l = 0 exactly when the row sees no token (a NaN score makes l NaN, and the row's o)
+    static_cast<__nv_bfloat16*>(p.o)[(size_t)blockIdx.x * D + tid] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+    if (tid == 0 && p.lse != nullptr) p.lse[blockIdx.x] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
+    return;
+  }
+  // A chunk's scores and weights; the first chunk's go out before the log-sum-exps are worked out.
+  float s[TPT][CP], w_in[TPT];
+  const int part1 = min(part0 + per_part, nv);
+  const float* sp = p.scores + ((size_t)unit * p.Lp + part0 + tid) * CP;
+  const size_t w0 = (size_t)unit * p.L + part0 + tid;
+  const float* wi = p.w_in != nullptr ? p.w_in + w0 : nullptr;
+  float* wo = p.w_out + w0;
+  auto load_chunk = [&](int n) {  // n: tokens of this thread's stride that are there
+#pragma unroll
+    for (int k = 0; k < TPT; ++k) {
+      w_in[k] = 0.f;
+      if (k * kJoinThreads < n) {
+        const float* q = sp + k * kJoinThreads * CP;
+        if constexpr (CP >= 4) {
+#pragma unroll
+          for (int c = 0; c < CP; c += 4) {
+            const float4 u = __ldcs(reinterpret_cast<const float4*>(q + c));
+            s[k][c] = u.x; s[k][c + 1] = u.y; s[k][c + 2] = u.z; s[k][c + 3] = u.w;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < CP; ++c) s[k][c] = q[c];
+        }
+        if (wi != nullptr) w_in[k] = wi[k * kJoinThreads];
+      }
+    }
+  };
+  int left = part1 - part0 - tid;
+  load_chunk(left);
+  for (int c = tid >> 5; c < CP; c += kJoinThreads / 32) {  // a warp per row
+    const int lane = tid & 31;
+    float M = -INFINITY, l = 0.f;
+    if (c < p.cols) {
+      for (int i = lane; i < np; i += 32) M = fmaxf(M, ml[(s0 + i) * p.cols + c].x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    }
+    const float base = M == -INFINITY ? 0.f : M;
+    if (c < p.cols) {
+      for (int i = lane; i < np; i += 32) {
+        const float2 x = ml[(s0 + i) * p.cols + c];
+        l = fmaf(x.y, exp2f(x.x - base), l);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    }
+    // Rows that see nothing have scores of -inf only, and rows past cols (whose scores mean nothing) add none.
+    if (lane == 0) slse[c] = c >= p.cols ? INFINITY : (l == 0.f ? 0.f : base + log2f(l));
+  }
+  __syncthreads();
+  float sub[CP];
+#pragma unroll
+  for (int c = 0; c < CP; ++c) sub[c] = slse[c];
+  for (;;) {
+#pragma unroll
+    for (int k = 0; k < TPT; ++k) {
+      float w = 0.f;
+#pragma unroll
+      for (int c = 0; c < CP; ++c)
+        if (CP < 4 || c < p.cols) w += tc::ex2_approx(s[k][c] - sub[c]);  // below 2^-126: 0
+      if (k * kJoinThreads < left) wo[k * kJoinThreads] = w_in[k] + w;
+    }
+    left -= CHUNK;
+    if (left + tid <= 0) break;
+    sp += CHUNK * CP;
+    if (wi != nullptr) wi += CHUNK;
+    wo += CHUNK;
+    load_chunk(left);
   }
 }
 
-// Adds each token's attention weight, summed over the unit's query rows in order.
-__global__ void __launch_bounds__(256) attn_weight_kernel(Cache8Attn p, int chunks) {
-  const int unit = blockIdx.x / chunks, b = unit / p.Hkv;
-  const int nv = visible(p.lens, b, p.L, p.back, nullptr);
-  const int t = (blockIdx.x % chunks) * 256 + threadIdx.x;
-  if (t >= nv) return;
-  const float* s = p.scores + (size_t)unit * p.cols * p.Lp + t;
-  float w = 0.f;
-  for (int c = 0; c < p.cols; ++c) {
-    const float x = s[(size_t)c * p.Lp];
-    if (x != -INFINITY) w += exp2f(x - p.lse2[unit * p.cols + c]);
+template <int D, int CP>
+static cudaError_t launch_join(const Cache8Attn& p, cudaStream_t st) {
+  // The weights part: CTAs of whole chunks, about four CTAs per SM in all (each pays its start once).
+  const int chunk = weight_tokens(CP) * kJoinThreads, chunks = (p.L + chunk - 1) / chunk;
+  const long long units = (long long)p.B * p.Hkv;
+  long long each = units * chunks / (4 * kSms);
+  each = each < 1 ? 1 : (each > chunks ? chunks : each);
+  const int parts = (int)((chunks + each - 1) / each);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.B * p.Hkv * (p.cols + (p.w_out != nullptr ? parts : 0)));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, CP>, p, parts, (int)each * chunk);
+}
+
+template <int D>
+static cudaError_t launch_join_d(const Cache8Attn& p, cudaStream_t st) {
+  switch (p.cpad) {
+    case 1: return launch_join<D, 1>(p, st);
+    case 2: return launch_join<D, 2>(p, st);
+    case 4: return launch_join<D, 4>(p, st);
+    case 8: return launch_join<D, 8>(p, st);
+    case 12: return launch_join<D, 12>(p, st);
+    default: return launch_join<D, 16>(p, st);
   }
-  const size_t at = (size_t)unit * p.L + t;
-  p.w_out[at] = p.w_in != nullptr ? p.w_in[at] + w : w;
 }
 
 // ---------------------------------------------------------------------------
@@ -185,14 +316,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_list_kernel(Cache8Attn p) {
 cudaError_t launch_cache8_attn(const Cache8Attn& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   cudaError_t e = launch_cache8_tiles(p, tk, tv, st);
   if (e != cudaSuccess) return e;
-  const unsigned rows = (unsigned)(p.B * p.Hkv * p.cols);
-  if (p.D == 128) attn_join_kernel<128><<<rows, 128, 0, st>>>(p);
-  else attn_join_kernel<64><<<rows, 64, 0, st>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || p.w_out == nullptr) return e;
-  const int chunks = (p.L + 255) / 256;
-  attn_weight_kernel<<<(unsigned)(chunks * p.B * p.Hkv), 256, 0, st>>>(p, chunks);
-  return cudaGetLastError();
+  return p.D == 128 ? launch_join_d<128>(p, st) : launch_join_d<64>(p, st);
 }
 
 cudaError_t launch_cache8_attn_list(const Cache8Attn& p, cudaStream_t st) {

@@ -2,7 +2,7 @@
 // tensor cores (the first of the two steps: pieces; cache8_attn.cu joins them).
 //
 // The codes go to the tensor core as they are (kind::f8f6f4), so no cached value
-// is converted by a thread.  Per tile of 128 tokens:
+// is converted by a thread.  Per 128 tokens:
 //   S^T [128 tokens, 2 NC] = K [128, D] . Q^T     Q: NC query rows (the group's heads x query tokens)
 //   O^T [D, 2 NC]          = V^T [D, 128] . P^T
 // A bf16 query row or a float32 probability does not fit 4 significant bits, so
@@ -16,18 +16,20 @@
 // scales that lie far apart between blocks lose nothing: the block's factor
 // 2^(max - running max) * v_scale is applied when O^T is added to the registers.
 //
-//   warps 0 .. 3  thread t = token t of the tile for S (TMEM lane t): scores, block
-//                 maximum (warp maxima through shared memory), probabilities as
-//                 e4m3 into shared memory; thread r = dim r for O^T: the running
-//                 O of the piece in registers.  O^T of tile j - 1 is added after
-//                 the probabilities of tile j are on their way.
+//   warps 0 .. 3  thread i = token i of the tile for S (TMEM lane i; i and i + 128 in
+//                 tiles of 256): scores, block maxima (warp maxima through shared
+//                 memory), probabilities as e4m3 into shared memory; thread r = dim r
+//                 for O^T: the running O of the piece in registers.  O^T of tile j - 1
+//                 is added after the probabilities of tile j are on their way.
 //   warp 4        producer: TMA tiles of K and V (a ring each)
 //   warp 5        MMA issuer
-// A tile of 128 tokens is 32 KB (d = 128) and 8 MMAs of N = 2 NC; the tensor core
-// is idle most of the time and the kernel's bound is the cache's bytes.
-// Work split, pieces and their slots: cache8.cuh.  Every wait is bounded; one that
-// runs out sets SFA_ERR_TIMEOUT and an abort flag, after which waits return at
-// once and the CTA runs to its end (the copies and MMAs it issued are drained).
+// A tile is 32 KB (128 tokens of d = 128, 256 of d = 64: with 128 tokens the softmax
+// warps, a chain of latencies, set the pace of the smaller rows) and 8 to 12 MMAs of
+// N = 2 NC; the tensor core is idle most of the time and the kernel's bound is the
+// cache's bytes.  Work split, pieces and their slots: cache8.cuh.  Every wait is
+// bounded; one that runs out sets SFA_ERR_TIMEOUT and an abort flag, after which
+// waits return at once and the CTA runs to its end (the copies and MMAs it issued
+// are drained).
 #include <cuda.h>
 #include <math.h>
 
@@ -40,34 +42,37 @@ namespace {
 
 using namespace c8;
 
+constexpr int kTileThreads = 192;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr int kEdge = kMaxCols - 1;   // tokens that not every query sees: nq - 1 at most
+constexpr int kEdge = kMaxCols - 1;  // tokens that not every query sees: nq - 1 at most
 constexpr float kLoQ = 16.f, kLoP = 32.f, kTopP = 256.f;
 
 template <int D, int NC, int T>
 struct Lay {
-  static constexpr int N = 2 * NC;                // MMA columns
-  static constexpr int SUB = kTile / T;           // scale blocks of a tile
-  static constexpr uint32_t TILE = kTile * D;     // bytes of a K or V tile
-  static constexpr int NK = D == 128 ? 3 : 6;     // ring stages of K, of V (16 rows leave less room)
-  static constexpr int NV = NC == 8 ? NK : NK - NK / 3;
-  static constexpr uint32_t QB = N * D, PB = kTile * N;
+  static constexpr int N = 2 * NC;                   // MMA columns
+  static constexpr int TILE_T = tile_tokens(D, NC);  // tokens of a tile
+  static constexpr int H = TILE_T / 128;             // tokens per softmax thread
+  static constexpr int SUBH = 128 / T;               // scale blocks of 128 tokens
+  static constexpr int SUB = H * SUBH;               // and of a tile
+  static constexpr uint32_t TILE = TILE_T * D;       // bytes of a K or V tile
+  static constexpr int STAGES = 49152 / TILE;        // 48 KB each for K and V
+  static constexpr int NK = STAGES, NV = NC == 8 ? STAGES : STAGES - STAGES / 3;  // 16 rows leave less room
+  static constexpr uint32_t QB = N * D, PB = TILE_T * N;
   static constexpr uint32_t OFF_K = 0, OFF_V = NK * TILE;
-  static constexpr uint32_t OFF_Q = (NK + NV) * TILE;            // two buffers
-  static constexpr uint32_t OFF_P = OFF_Q + 2 * QB;              // two buffers
-  static constexpr uint32_t OFF_EV = OFF_P + 2 * PB;             // edge tokens' V rows, two buffers
-  static constexpr uint32_t OFF_EE = OFF_EV + 2 * kEdge * D;     // their probabilities [2][kEdge][NC]
-  static constexpr uint32_t OFF_MAX = OFF_EE + 2 * kEdge * NC * 4;   // warp maxima [2][4][NC]
-  static constexpr uint32_t OFF_FAC = OFF_MAX + 2 * 4 * NC * 4;      // [2][NC] keep, [2][SUB][NC] f, [2][SUB][NC] f v
+  static constexpr uint32_t OFF_Q = (NK + NV) * TILE;                // two buffers
+  static constexpr uint32_t OFF_P = OFF_Q + 2 * QB;                  // two buffers
+  static constexpr uint32_t OFF_EV = OFF_P + 2 * PB;                 // edge tokens' V rows, two buffers
+  static constexpr uint32_t OFF_EE = OFF_EV + 2 * kEdge * D;         // their probabilities [2][kEdge][NC]
+  static constexpr uint32_t OFF_MAX = OFF_EE + 2 * kEdge * NC * 4;   // warp maxima [2][H][4][NC]
+  static constexpr uint32_t OFF_FAC = OFF_MAX + 2 * H * 4 * NC * 4;  // [2][NC] keep, [2][SUB][NC] f, [2][SUB][NC] f v
   static constexpr uint32_t OFF_QF = OFF_FAC + 2 * NC * (1 + 2 * SUB) * 4;  // row factors [2][NC]
   static constexpr uint32_t OFF_BAR = OFF_QF + 2 * NC * 4;
-  static constexpr int NBAR = 2 * NK + 2 * NV + 9;
+  static constexpr int B0 = 2 * NK + 2 * NV, NBAR = B0 + 9;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t BYTES = OFF_MISC + 64 + 1024;
-  // TMEM columns: S two buffers, O two buffers x SUB
-  static constexpr uint32_t COL_O = 2 * N, COLS_USED = 2 * N + 2 * SUB * N;
+  // TMEM columns: S two buffers of H parts, O two buffers of SUB parts
+  static constexpr uint32_t COL_O = 2 * H * N, COLS_USED = COL_O + 2 * SUB * N;
   static constexpr uint32_t TMEM = COLS_USED <= 64 ? 64 : (COLS_USED <= 128 ? 128 : 256);
-  static constexpr int B0 = 2 * NK + 2 * NV;
   __host__ __device__ static constexpr int kf(int s) { return s; }
   __host__ __device__ static constexpr int ke(int s) { return NK + s; }
   __host__ __device__ static constexpr int vf(int s) { return 2 * NK + s; }
@@ -108,22 +113,24 @@ __device__ void drain(uint32_t bar, uint32_t parity) {
 }
 
 // The pieces of a CTA's share, in order.
+template <int TILE_T>
 struct Pieces {
-  long long left;  // tiles of the share after the present piece
+  int left;                   // tiles of the share after the present piece
   int b, g, nv, first, last;  // unit (b, g), its visible tokens, the piece's tiles [first, last)
 
-  __device__ void begin(const Cache8Attn& p, int b0, long long x0, long long before, long long n) {
+  // `skip`: tiles of sequence b0 before the share; nv0: its visible tokens.
+  __device__ void begin(int b0, int skip, int nv0, int n) {
     b = b0;
-    nv = visible(p.lens, b, p.L, p.back, nullptr);
-    const int tiles = (nv + kTile - 1) / kTile;
-    g = (int)((x0 - before) / tiles);
-    first = (int)((x0 - before) % tiles);
-    last = (int)min((long long)tiles, first + n);
+    nv = nv0;
+    const int tiles = (nv + TILE_T - 1) / TILE_T;
+    g = skip / tiles;
+    first = skip % tiles;
+    last = min(tiles, first + n);
     left = n - (last - first);
   }
   __device__ bool next(const Cache8Attn& p) {
     if (left <= 0) return false;
-    int tiles = (nv + kTile - 1) / kTile;
+    int tiles = (nv + TILE_T - 1) / TILE_T;
     if (++g == p.Hkv) {
       g = 0;
       do {
@@ -132,15 +139,32 @@ struct Pieces {
           return false;
         }
         nv = visible(p.lens, b, p.L, p.back, nullptr);
-        tiles = (nv + kTile - 1) / kTile;
-      } while (tiles == 0);  // `left` tiles follow, so a sequence with tiles does
+        tiles = (nv + TILE_T - 1) / TILE_T;
+      } while (tiles == 0);
     }
     first = 0;
-    last = (int)min((long long)tiles, left);
+    last = min(tiles, left);
     left -= last;
     return true;
   }
 };
+
+// NC consecutive floats of shared memory, 16 bytes a load.
+template <int NC>
+__device__ __forceinline__ void load_row(const float* p, float (&v)[NC]) {
+#pragma unroll
+  for (int c = 0; c < NC; c += 4) {
+    const float4 u = *reinterpret_cast<const float4*>(p + c);
+    v[c] = u.x; v[c + 1] = u.y; v[c + 2] = u.z; v[c + 3] = u.w;
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_row(uint32_t at, uint32_t (&v)[N]) {
+  static_assert(N == 16 || N == 32, "two columns a query row");
+  if constexpr (N == 16) tc::tmem_ld16(at, v);
+  else tc::tmem_ld32(at, v);
+}
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -191,18 +215,18 @@ __device__ __forceinline__ void write_q(const Cache8Attn& p, unsigned char* sm, 
 }
 
 template <int D, int NC, int T>
-__global__ void __launch_bounds__(192, 2)
+__global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
     attn_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ Cache8Attn p) {
   using L = Lay<D, NC, T>;
-  constexpr int N = L::N, SUB = L::SUB, NK = L::NK, NV = L::NV;
+  constexpr int N = L::N, H = L::H, SUB = L::SUB, SUBH = L::SUBH, NK = L::NK, NV = L::NV, TILE_T = L::TILE_T;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = tc::smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
   unsigned char* sm = smem_raw + pad;
   const uint32_t sb = raw + pad;
-  long long* sched = reinterpret_cast<long long*>(sm + L::OFF_MISC);  // before, x0, tiles of the share
-  int* sched_b = reinterpret_cast<int*>(sm + L::OFF_MISC + 24);
+  int* sched = reinterpret_cast<int*>(sm + L::OFF_MISC);  // first sequence, its tiles before the share, the
+                                                          // share's tiles, the sequence's visible tokens
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::OFF_MISC + 28);
   Ctx cx;
   cx.bars = sb + L::OFF_BAR;
@@ -210,19 +234,16 @@ __global__ void __launch_bounds__(192, 2)
   cx.status = p.status;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining step waits for this grid's end itself
   if (warp == 0) {
-    long long dummy, before = 0;
-    const long long total = warp_count_tiles(p.lens, p.B, p.Hkv, p.L, p.back, 0, &dummy,
-                                             blockIdx.x == 0 ? p.status : nullptr);
-    const Split s(total, p.G);
-    const long long x0 = s.start(blockIdx.x), n = s.start(blockIdx.x + 1) - x0;
-    int b = -1;
-    if (n > 0) b = warp_find_seq(p.lens, p.B, p.Hkv, p.L, p.back, x0, &before);
+    int b, skip;
+    const int n = warp_share(p.lens, p.B, p.Hkv, p.L, p.back, TILE_T, p.G, blockIdx.x, &b, &skip,
+                             blockIdx.x == 0 ? p.status : nullptr);
     if (lane == 0) {
-      sched[0] = before;
-      sched[1] = x0;
-      sched[2] = b < 0 ? 0 : n;
-      *sched_b = b;
+      sched[0] = b;
+      sched[1] = skip;
+      sched[2] = n;
+      sched[3] = visible(p.lens, b, p.L, p.back, nullptr);
     }
   } else if (warp == 4 && lane == 0) {
     *cx.abort_flag = 0;
@@ -239,30 +260,33 @@ __global__ void __launch_bounds__(192, 2)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const long long n = sched[2];
+  const int n = sched[2];
 
   if (n > 0) {
-    Pieces pc;
-    pc.begin(p, *sched_b, sched[1], sched[0], n);
+    Pieces<TILE_T> pc;
+    pc.begin(sched[0], sched[1], sched[3], n);
     if (warp == 4) {
       // ------------------------------ producer ------------------------------
       if (lane == 0) {
         uint32_t j = 0;
         bool ok = true;
+        const uint64_t once = tc::policy_evict_first();  // leaves L2 to the scores, queries and pieces (2%)
         do {
           const int row0 = (pc.b * p.Hkv + pc.g) * p.L;
           for (int t = pc.first; ok && t < pc.last; ++t, ++j) {
             const uint32_t sk = j % NK, sv = j % NV;
             if (j >= NK && !wait(cx, cx.bar(L::ke(sk)), ((j / NK) & 1) ^ 1)) { ok = false; break; }
             tc::mbar_arrive_expect_tx(cx.bar(L::kf(sk)), L::TILE);
-            tc::tma_load_2d(sb + L::OFF_K + sk * L::TILE, &tmK, cx.bar(L::kf(sk)), 0, row0 + t * kTile);
+            tc::tma_load_2d_hint(sb + L::OFF_K + sk * L::TILE, &tmK, cx.bar(L::kf(sk)), 0, row0 + t * TILE_T,
+                                 once);
             if (j >= NV && !wait(cx, cx.bar(L::ve(sv)), ((j / NV) & 1) ^ 1)) {
               drain(cx.bar(L::kf(sk)), (j / NK) & 1);
               ok = false;
               break;
             }
             tc::mbar_arrive_expect_tx(cx.bar(L::vf(sv)), L::TILE);
-            tc::tma_load_2d(sb + L::OFF_V + sv * L::TILE, &tmV, cx.bar(L::vf(sv)), 0, row0 + t * kTile);
+            tc::tma_load_2d_hint(sb + L::OFF_V + sv * L::TILE, &tmV, cx.bar(L::vf(sv)), 0, row0 + t * TILE_T,
+                                 once);
           }
         } while (ok && pc.next(p));
         if (*cx.abort_flag) {  // every copy that was started lands before the CTA exits
@@ -296,9 +320,11 @@ __global__ void __launch_bounds__(192, 2)
           tc::tc_fence_after();
           const uint32_t k = sb + L::OFF_K + s * L::TILE, q = sb + L::OFF_Q + qbuf * L::QB;
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-            tc::mma_e4m3_ss(tmem + (j & 1) * N, tc::smem_desc(k + i * 32, 16, ROWS8, SWZ),
-                            tc::smem_desc(q + i * 256, 128, D * 8, 0), id_qk, i > 0);
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+              tc::mma_e4m3_ss(tmem + ((j & 1) * H + h) * N, tc::smem_desc(k + h * 128 * D + i * 32, 16, ROWS8, SWZ),
+                              tc::smem_desc(q + i * 256, 128, D * 8, 0), id_qk, i > 0);
           tc::mma_commit(cx.bar(L::ke(s)));
           tc::mma_commit(cx.bar(L::sf(j & 1)));
           return true;
@@ -315,12 +341,10 @@ __global__ void __launch_bounds__(192, 2)
           tc::tc_fence_after();
           const uint32_t v = sb + L::OFF_V + s * L::TILE, pp = sb + L::OFF_P + (j & 1) * L::PB;
 #pragma unroll
-          for (int i = 0; i < kTile / 32; ++i) {
-            const int sub = i / (T / 32);
-            tc::mma_e4m3_ss(tmem + L::COL_O + ((j & 1) * SUB + sub) * N,
+          for (int i = 0; i < TILE_T / 32; ++i)
+            tc::mma_e4m3_ss(tmem + L::COL_O + ((j & 1) * SUB + i / (T / 32)) * N,
                             tc::smem_desc(v + i * 4 * ROWS8, ROWS8, ROWS8, SWZ),
-                            tc::smem_desc(pp + i * 512, 128, 2048, 0), id_pv, i % (T / 32) > 0);
-          }
+                            tc::smem_desc(pp + i * 512, 128, TILE_T * 16, 0), id_pv, i % (T / 32) > 0);
           tc::mma_commit(cx.bar(L::ve(s)));
           tc::mma_commit(cx.bar(L::of(j & 1)));
           if (j + 2 < tiles) ok = issue_s(j + 2);
@@ -330,201 +354,271 @@ __global__ void __launch_bounds__(192, 2)
       }
     } else {
       // ------------------------- softmax and O ------------------------------
-      float* smax = reinterpret_cast<float*>(sm + L::OFF_MAX);    // [2][4][NC]
+      float* smax = reinterpret_cast<float*>(sm + L::OFF_MAX);    // [2][H][4][NC]
       float* fkeep = reinterpret_cast<float*>(sm + L::OFF_FAC);   // [2][NC]
       float* ff = fkeep + 2 * NC;                                 // [2][SUB][NC]
       float* ffv = ff + 2 * SUB * NC;                             // [2][SUB][NC]
       float* ee = reinterpret_cast<float*>(sm + L::OFF_EE);       // [2][kEdge][NC]
       const float* qfac = reinterpret_cast<const float*>(sm + L::OFF_QF);
       const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-      const int sub = tid / T;
       constexpr int WPS = T / 32;  // warps per scale block
+      const int my_sub = tid / T;  // scale block of this thread's token within its 128
+      // Lane fs NC + fc of warp 0 keeps row fc's running maximum and works out its factor for block fs.
+      const int fc = lane % NC, fs = lane / NC;
+      const bool factors = warp == 0 && fs < SUB;
       uint32_t j = 0, piece = 0;
 
       write_q<D, NC, T>(p, sm, 0, pc.b * p.Hkv + pc.g, tid);
       tc::fence_proxy_async_smem();
       tc::mbar_arrive(cx.bar(L::qf(0)));
-      Pieces nx = pc;
-      bool more = nx.next(p);
+      Pieces<TILE_T> nx = pc;
+      bool more;
       for (;;) {
         const int unit = pc.b * p.Hkv + pc.g;
-        if (more) {  // the next piece's query rows, a piece ahead of their first use
-          write_q<D, NC, T>(p, sm, (piece + 1) & 1, nx.b * p.Hkv + nx.g, tid);
-          tc::fence_proxy_async_smem();
-          tc::mbar_arrive(cx.bar(L::qf((piece + 1) & 1)));
-        }
+        const int blk0 = unit * p.nblk;  // B Hkv blocks stay under 2^31
+        // The scales of a tile are loaded a tile ahead.
+        float ks_next[H], vs_next = 0.f;
+        auto load_scales = [&](int tile) {
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            const int t = tile * TILE_T + h * 128 + tid;
+            ks_next[h] = t < pc.nv ? __ldg(p.ks + blk0 + t / T) : 0.f;
+          }
+          const int tv = tile * TILE_T + fs * T;
+          if (factors) vs_next = tv < pc.nv ? __ldg(p.vs + blk0 + tv / T) * (1.f / kTopP) : 0.f;
+        };
+        load_scales(pc.first);
         softmax_sync();  // this piece's row factors, written by other warps
-        float qf[NC], l[NC], acc[NC], e_prev[NC];
+        float l[NC], acc[NC], e_prev[H][NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          qf[c] = qfac[(piece & 1) * NC + c];
-          l[c] = acc[c] = e_prev[c] = 0.f;
+          l[c] = acc[c] = 0.f;
+#pragma unroll
+          for (int h = 0; h < H; ++h) e_prev[h][c] = 0.f;
         }
-        float M = -INFINITY;  // threads 0 .. NC - 1: running maximum of row tid
-        int edge_prev = kTile;  // first edge token of the previous tile
-        int edge_n = 0;         // and how many
+        float M = -INFINITY;     // running maximum of row fc
+        int edge_prev = TILE_T;  // first edge token of the previous tile
+        int edge_n = 0;          // and how many
         // Adds O^T of tile i to the registers, and the tile's probabilities to l.
         auto absorb = [&](uint32_t i) {
           wait(cx, cx.bar(L::of(i & 1)), (i >> 1) & 1);
           __syncwarp();
           tc::tc_fence_after();
-          const float* kp = fkeep + (i & 1) * NC;
-          const float* fp = ff + ((i & 1) * SUB + sub) * NC;
-          const float* vp = ffv + (i & 1) * SUB * NC;
+          constexpr int BOTH = NC == 8 && SUB > 1 ? 2 : 1;  // blocks loaded at once (16 rows: registers for one)
+          uint32_t o[BOTH][N];
+          const uint32_t at = tmem + lane_base + L::COL_O + (i & 1) * SUB * N;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const float k = kp[c];
-            acc[c] *= k;
-            l[c] = fmaf(e_prev[c], fp[c], l[c] * k);
+          for (int s = 0; s < BOTH; ++s) tmem_row<N>(at + s * N, o[s]);
+          {
+            float kp[NC];
+            load_row<NC>(fkeep + (i & 1) * NC, kp);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              acc[c] *= kp[c];
+              l[c] *= kp[c];
+            }
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              float fp[NC];
+              load_row<NC>(ff + ((i & 1) * SUB + h * SUBH + my_sub) * NC, fp);
+#pragma unroll
+              for (int c = 0; c < NC; ++c) l[c] = fmaf(e_prev[h][c], fp[c], l[c]);
+            }
           }
-          if (D == 128 || warp < 2) {
+          const float* vp = ffv + (i & 1) * SUB * NC;
+          // d = 64: lanes 64 .. 127 hold copies of other rows (the MMA has 128) that are never written out.
 #pragma unroll
-            for (int s = 0; s < SUB; ++s) {
-              uint32_t o[N];
-              const uint32_t at = tmem + lane_base + L::COL_O + ((i & 1) * SUB + s) * N;
-              if constexpr (N == 16) tc::tmem_ld16(at, o); else tc::tmem_ld32(at, o);
-              tc::tmem_wait_ld();
+          for (int s0 = 0; s0 < SUB; s0 += BOTH) {
+            if (s0 > 0) {
+#pragma unroll
+              for (int s = 0; s < BOTH; ++s) tmem_row<N>(at + (s0 + s) * N, o[s]);
+            }
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int s = 0; s < BOTH; ++s) {
+              float fv[NC];
+              load_row<NC>(vp + (s0 + s) * NC, fv);
 #pragma unroll
               for (int c = 0; c < NC; ++c)
-                acc[c] = fmaf(fmaf(__uint_as_float(o[NC + c]), 1.f / kLoP, __uint_as_float(o[c])), vp[s * NC + c],
+                acc[c] = fmaf(fmaf(__uint_as_float(o[s][NC + c]), 1.f / kLoP, __uint_as_float(o[s][c])), fv[c],
                               acc[c]);
             }
-            for (int r = 0; r < edge_n; ++r) {
-              const float v = __low2float(from_e4m3x2(sm[L::OFF_EV + ((i & 1) * kEdge + r) * D + tid])) * kTopP;
-              const float* er = ee + ((i & 1) * kEdge + r) * NC;
-              const float* vr = vp + ((edge_prev + r) / T) * NC;
+          }
+          for (int r = 0; r < edge_n; ++r) {
+            const float v = __low2float(from_e4m3x2(sm[L::OFF_EV + ((i & 1) * kEdge + r) * D + tid % D])) * kTopP;
+            const float* er = ee + ((i & 1) * kEdge + r) * NC;
+            const float* vr = vp + ((edge_prev + r) / T) * NC;
 #pragma unroll
-              for (int c = 0; c < NC; ++c)
-                if (!(er[c] < 0.f)) acc[c] = fmaf(er[c] * vr[c], v, acc[c]);  // < 0: the row does not see it
-            }
+            for (int c = 0; c < NC; ++c)
+              if (!(er[c] < 0.f)) acc[c] = fmaf(er[c] * vr[c], v, acc[c]);  // < 0: the row does not see it
           }
           tc::tc_fence_before();
         };
 
         for (int tile = pc.first; tile < pc.last; ++tile, ++j) {
-          const int t = tile * kTile + tid;
-          const bool live = t < pc.nv;
-          const float ks = live ? __ldg(p.ks + (size_t)unit * p.nblk + t / T) : 0.f;
-          float vs[SUB];
-          if (tid < NC) {
+          const int t0 = tile * TILE_T;
+          const int edge = max(pc.nv - p.nq + 1 - t0, 0);  // tokens from here on: not seen by every row
+          float ks[H];
 #pragma unroll
-            for (int s = 0; s < SUB; ++s) {
-              const int t0 = tile * kTile + s * T;
-              vs[s] = t0 < pc.nv ? __ldg(p.vs + (size_t)unit * p.nblk + t0 / T) * (1.f / kTopP) : 0.f;
-            }
-          }
+          for (int h = 0; h < H; ++h) ks[h] = ks_next[h];
+          const float vs = vs_next;
+          if (tile + 1 < pc.last) load_scales(tile + 1);
           wait(cx, cx.bar(L::sf(j & 1)), (j >> 1) & 1);
           __syncwarp();
           tc::tc_fence_after();
-          float e[NC];
+          float e[H][NC];  // scores in log2 units, then probabilities against the block's maximum
           {
-            uint32_t r[N];
-            if constexpr (N == 16) tc::tmem_ld16(tmem + lane_base + (j & 1) * N, r);
-            else tc::tmem_ld32(tmem + lane_base + (j & 1) * N, r);
-            tc::tmem_wait_ld();
+            float qf[NC];
+            load_row<NC>(qfac + (piece & 1) * NC, qf);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              const float s = fmaf(__uint_as_float(r[NC + c]), 1.f / kLoQ, __uint_as_float(r[c])) * (ks * qf[c]);
-              const bool sees = c < p.cols && t < pc.nv - (p.nq - 1 - c % p.nq);
-              e[c] = sees ? s : -INFINITY;
+            for (int h = 0; h < H; ++h) {
+              uint32_t r[N];
+              tmem_row<N>(tmem + lane_base + ((j & 1) * H + h) * N, r);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < NC; ++c)
+                e[h][c] = fmaf(__uint_as_float(r[NC + c]), 1.f / kLoQ, __uint_as_float(r[c])) * (ks[h] * qf[c]);
             }
           }
-          float* wm = smax + (j & 1) * 4 * NC;
-          {
+          if (edge < TILE_T) {  // only here some row does not see some token; rows from cols on are never used
+            for (int i = 0; i < p.nq; ++i) {
+#pragma unroll
+              for (int h = 0; h < H; ++h) {
+                const bool sees = t0 + h * 128 + tid < pc.nv - (p.nq - 1 - i);
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                  if (!sees && c % p.nq == i) e[h][c] = -INFINITY;
+              }
+            }
+          }
+          float* wm = smax + (j & 1) * H * 4 * NC;
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
             float mine = 0.f;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-              const float m = tc::warp_max(e[c]);
+              const float m = tc::warp_max(e[h][c]);
               if (lane == c) mine = m;
             }
-            if (lane < NC) wm[warp * NC + lane] = mine;
+            if (lane < NC) wm[(h * 4 + warp) * NC + lane] = mine;
           }
-          if (p.scores != nullptr && live) {
-            float* sc = p.scores + (size_t)unit * p.cols * p.Lp + t;
+          if (p.scores != nullptr) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if (c < p.cols) sc[(size_t)c * p.Lp] = e[c];
+            for (int h = 0; h < H; ++h) {
+              const int t = t0 + h * 128 + tid;
+              if (t >= pc.nv) continue;
+              float* sc = p.scores + ((size_t)unit * p.Lp + t) * p.cpad;
+              if (p.cpad >= 4) {
+#pragma unroll
+                for (int c = 0; c < NC; c += 4)
+                  if (c < p.cpad)
+                    *reinterpret_cast<float4*>(sc + c) = make_float4(e[h][c], e[h][c + 1], e[h][c + 2], e[h][c + 3]);
+              } else if (p.cpad == 2) {
+                *reinterpret_cast<float2*>(sc) = make_float2(e[h][0], e[h][1]);
+              } else {
+                *sc = e[h][0];
+              }
+            }
           }
           softmax_sync();
-          const int edge = max(pc.nv - p.nq + 1 - tile * kTile, 0);  // tokens from here on: not seen by every row
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            float m = -INFINITY;
+          for (int h = 0; h < H; ++h) {
+            float m[NC];
+            load_row<NC>(wm + (h * 4 + my_sub * WPS) * NC, m);
 #pragma unroll
-            for (int w = 0; w < WPS; ++w) m = fmaxf(m, wm[(sub * WPS + w) * NC + c]);
-            const float x = e[c];
-            e[c] = tc::ex2_approx(x - (m == -INFINITY ? 0.f : m));
-          }
-          if (tid < NC) {  // factors of row tid: running maximum, this tile's blocks against it
-            float mt[SUB], mn = M;
+            for (int w = 1; w < WPS; ++w) {
+              float u[NC];
+              load_row<NC>(wm + (h * 4 + my_sub * WPS + w) * NC, u);
 #pragma unroll
-            for (int s = 0; s < SUB; ++s) {
-              mt[s] = -INFINITY;
-#pragma unroll
-              for (int w = 0; w < WPS; ++w) mt[s] = fmaxf(mt[s], wm[(s * WPS + w) * NC + tid]);
-              mn = fmaxf(mn, mt[s]);
+              for (int c = 0; c < NC; ++c) m[c] = fmaxf(m[c], u[c]);
             }
-            fkeep[(j & 1) * NC + tid] = M == -INFINITY ? 0.f : exp2f(M - mn);
 #pragma unroll
-            for (int s = 0; s < SUB; ++s) {
-              const float f = mt[s] == -INFINITY ? 0.f : exp2f(mt[s] - mn);
-              ff[((j & 1) * SUB + s) * NC + tid] = f;
-              ffv[((j & 1) * SUB + s) * NC + tid] = f * vs[s];
-            }
-            M = mn;
+            for (int c = 0; c < NC; ++c) e[h][c] = tc::ex2_approx(e[h][c] - (m[c] == -INFINITY ? 0.f : m[c]));
           }
           // Probabilities as two e4m3 parts: B operand, MN-major, no swizzle (8 tokens x 16 rows contiguous).
-          {
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
             uint32_t hi[NC / 4], lo[NC / 4];
 #pragma unroll
             for (int c = 0; c < NC; c += 4) {
               uint32_t h2[2], l2[2];
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
-                const float a = e[c + 2 * u] * kTopP, b = e[c + 2 * u + 1] * kTopP;
+                const float a = e[h][c + 2 * u] * kTopP, b = e[h][c + 2 * u + 1] * kTopP;
                 h2[u] = to_e4m3x2(a, b);
-                const float2 h = __half22float2(from_e4m3x2(h2[u]));
-                l2[u] = to_e4m3x2((a - h.x) * kLoP, (b - h.y) * kLoP);
+                const float2 f = __half22float2(from_e4m3x2(h2[u]));
+                l2[u] = to_e4m3x2((a - f.x) * kLoP, (b - f.y) * kLoP);
               }
               hi[c / 4] = h2[0] | (h2[1] << 16);
               lo[c / 4] = l2[0] | (l2[1] << 16);
             }
-            unsigned char* pp = sm + L::OFF_P + (j & 1) * L::PB + tid * 16;
+            unsigned char* pp = sm + L::OFF_P + (j & 1) * L::PB + (h * 128 + tid) * 16;
             if constexpr (NC == 8) {
               *reinterpret_cast<uint4*>(pp) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
             } else {
               *reinterpret_cast<uint4*>(pp) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(pp + 2048) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              *reinterpret_cast<uint4*>(pp + TILE_T * 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
           }
-          if (edge < kTile) {
+          if (edge < TILE_T) {
             // Rows of V that some query must not see: a NaN there would pass through a zero probability.  Rows behind
             // the last token become 0; the few that only the later queries see move aside and are added by hand.
             wait(cx, cx.bar(L::vf(j % NV)), (j / NV) & 1);
             __syncwarp();
-            if (tid >= edge) {
-              uint4* row = reinterpret_cast<uint4*>(sm + L::OFF_V + (j % NV) * L::TILE + tid * D);
-              if (live) {
-                uint4* ev = reinterpret_cast<uint4*>(sm + L::OFF_EV + ((j & 1) * kEdge + tid - edge) * D);
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) ev[i] = row[i ^ (D == 128 ? (tid & 7) : ((tid >> 1) & 3))];
-                float* er = ee + ((j & 1) * kEdge + tid - edge) * NC;
+            for (int h = 0; h < H; ++h) {
+              const int i = h * 128 + tid, t = t0 + i;
+              if (i < edge) continue;
+              uint4* row = reinterpret_cast<uint4*>(sm + L::OFF_V + (j % NV) * L::TILE + i * D);
+              if (t < pc.nv) {
+                uint4* ev = reinterpret_cast<uint4*>(sm + L::OFF_EV + ((j & 1) * kEdge + i - edge) * D);
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
-                  er[c] = c < p.cols && t < pc.nv - (p.nq - 1 - c % p.nq) ? e[c] : -1.f;
+                for (int k = 0; k < D / 16; ++k) ev[k] = row[k ^ (D == 128 ? (i & 7) : ((i >> 1) & 3))];
+                float* er = ee + ((j & 1) * kEdge + i - edge) * NC;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) er[c] = t < pc.nv - (p.nq - 1 - c % p.nq) ? e[h][c] : -1.f;
               }
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i) row[i] = make_uint4(0, 0, 0, 0);
+              for (int k = 0; k < D / 16; ++k) row[k] = make_uint4(0, 0, 0, 0);
             }
           }
           tc::fence_proxy_async_smem();
           tc::tc_fence_before();
           tc::mbar_arrive(cx.bar(L::pf(j & 1)));
-          if (tile > pc.first) absorb(j - 1);
+          if (warp == 0) {  // factors of row fc: the new running maximum, block fs against it
+            float mt = -INFINITY;
+            if (factors) {
 #pragma unroll
-          for (int c = 0; c < NC; ++c) e_prev[c] = e[c];
+              for (int w = 0; w < WPS; ++w) mt = fmaxf(mt, wm[(fs * WPS + w) * NC + fc]);
+            }
+            float mn = fmaxf(M, mt);
+#pragma unroll
+            for (int o = NC; o < NC * SUB; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+            if (factors) {
+              const float f = mt == -INFINITY ? 0.f : tc::ex2_approx(mt - mn);
+              if (fs == 0) fkeep[(j & 1) * NC + fc] = M == -INFINITY ? 0.f : tc::ex2_approx(M - mn);
+              ff[((j & 1) * SUB + fs) * NC + fc] = f;
+              ffv[((j & 1) * SUB + fs) * NC + fc] = f * vs;
+            }
+            M = mn;
+          }
+          if (tile == pc.first) {  // the next piece's query rows, ahead of their first use
+            nx = pc;
+            more = nx.next(p);
+            if (more) {
+              write_q<D, NC, T>(p, sm, (piece + 1) & 1, nx.b * p.Hkv + nx.g, tid);
+              tc::fence_proxy_async_smem();
+              tc::mbar_arrive(cx.bar(L::qf((piece + 1) & 1)));
+            }
+          } else {
+            absorb(j - 1);
+          }
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) e_prev[h][c] = e[h][c];
           edge_prev = edge;
-          edge_n = max(min(pc.nv - tile * kTile, kTile) - edge, 0);
+          edge_n = max(min(pc.nv - t0, TILE_T) - edge, 0);
         }
         softmax_sync();
         absorb(j - 1);
@@ -539,12 +633,11 @@ __global__ void __launch_bounds__(192, 2)
           if (c < p.cols && tid < D) p.part_o[(slot * p.cols + c) * D + tid] = acc[c];
         }
         softmax_sync();
-        if (tid < p.cols)
+        if (tid < p.cols)  // warp 0, lanes of block 0
           reinterpret_cast<float2*>(p.part_ml)[slot * p.cols + tid] =
               make_float2(M, (smax[tid] + smax[NC + tid]) + (smax[2 * NC + tid] + smax[3 * NC + tid]));
         if (!more) break;
         pc = nx;
-        more = nx.next(p);
         ++piece;
       }
     }
@@ -560,13 +653,15 @@ __global__ void __launch_bounds__(192, 2)
 template <int D, int NC, int T>
 cudaError_t launch_t(const Cache8Attn& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   using L = Lay<D, NC, T>;
-  static_assert(2 * (L::BYTES + 1024) <= 227 * 1024, "two CTAs per SM");
+  static_assert(kCtasPerSm * (L::BYTES + 1024) <= 228 * 1024, "shared memory of an SM");
+  static_assert(kCtasPerSm * L::TMEM <= 512, "tensor memory of an SM");
+  static_assert(L::SUB * NC <= 32, "a lane of warp 0 for each factor");
   auto kern = attn_tile_kernel<D, NC, T>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   if (e != cudaSuccess) return e;
-  kern<<<p.G, 192, L::BYTES, st>>>(tk, tv, p);
+  kern<<<p.G, kTileThreads, L::BYTES, st>>>(tk, tv, p);
   return cudaGetLastError();
 }
 

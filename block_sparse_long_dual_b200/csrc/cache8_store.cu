@@ -1,5 +1,7 @@
 // 8-bit KV cache: quantising rows into it, eviction by accumulated weight, and
 // the compact dominant-pair copy of its keys.
+#include <cooperative_groups.h>
+
 #include "cache8.cuh"
 
 namespace sfa {
@@ -7,6 +9,7 @@ namespace sfa {
 namespace {
 
 using namespace c8;
+namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
 
@@ -111,113 +114,193 @@ __global__ void advance_kernel(Cache8Append p) {
 }
 
 // ---------------------------------------------------------------------------
-// evict, selection: a CTA per (b, KV head).  Radix select (11 + 11 + 10 bits)
-// of the order-preserving weight keys, then the kept rows written in order.
+// evict, selection: a cluster of CS CTAs per (b, KV head), each over a contiguous
+// slice of the tokens.  Radix select (11 + 11 + 10 bits) of the order-preserving
+// weight keys: the slices' histograms are summed through distributed shared
+// memory, so every CTA finds the same threshold; a slice's own histograms also
+// tell how many kept rows lie before the next one.  A thread holds up to kKeys
+// consecutive keys in registers through all passes (a longer slice is read again
+// in each pass), so the kept rows leave in order after one scan.
+// Accumulated weights share few leading bits, so neighbouring lanes would queue on
+// one bin: four copies of the histogram, one per lane mod 4.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
+constexpr int kKeys = 16;
+constexpr int kBins = 2048;
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(Cache8Evict p) {
-  __shared__ int hist[2048];
-  __shared__ int wsum[32];
-  __shared__ int sh_digit, sh_above;
-  const int unit = blockIdx.x, b = unit / p.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Exclusive sum over the block of a 32-bit value, and the total.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* wsum, uint32_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  __syncthreads();  // wsum may still be read from the call before
+  if (lane == 31) wsum[warp] = inc;
+  __syncthreads();
+  const uint32_t w = wsum[lane];
+  *total = __reduce_add_sync(0xffffffffu, w);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u) + inc - x;
+}
+
+template <int CS>
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ Cache8Evict p) {
+  extern __shared__ uint32_t hist_raw[];
+  uint32_t (*hist)[kBins] = reinterpret_cast<uint32_t (*)[kBins]>(hist_raw);  // [4][kBins]
+  __shared__ uint32_t fold[2][kBins];
+  __shared__ uint32_t wsum[32];
+  __shared__ uint32_t share[2];  // this slice's keys above and at the threshold
+  __shared__ uint32_t sh_digit, sh_above;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = CS == 1 ? 0 : (int)cluster.block_rank();
+  const int unit = blockIdx.x / CS, b = unit / p.Hkv, tid = threadIdx.x;
   int n = p.lens[b];
   if (n < 0 || n > p.L) {
     if (tid == 0) report(p.status, SFA_ERR_INDEX);
     n = 0;
   }
   int* out = p.idx + (size_t)unit * p.keep;
-  const int kept = n < p.keep ? n : p.keep;
-  if (unit % p.Hkv == 0 && tid == 0) p.dlens[b] = kept;
+  if (unit % p.Hkv == 0 && rank == 0 && tid == 0) p.dlens[b] = n < p.keep ? n : p.keep;
   if (n <= p.keep) {
-    for (int i = tid; i < p.keep; i += kSelThreads) out[i] = i < n ? i : -1;
+    for (int i = rank * kSelThreads + tid; i < p.keep; i += CS * kSelThreads) out[i] = i < n ? i : -1;
     return;
   }
   const int old = n - p.recent, want = p.keep - p.recent;
-  const float* w = p.weight + (size_t)unit * p.L;
-  for (int i = tid; i < p.recent; i += kSelThreads) out[want + i] = old + i;
+  for (int i = rank * kSelThreads + tid; i < p.recent; i += CS * kSelThreads) out[want + i] = old + i;
   if (want == 0) return;
 
-  uint32_t prefix = 0;
-  int need = want;  // how many of the keys that match the prefix are kept
-  const int shift[4] = {21, 10, 0, 0}, bits[3] = {11, 11, 10};
-  for (int pass = 0; pass < 3; ++pass) {
-    const int nb = 1 << bits[pass];
-    for (int i = tid; i < nb; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < old; i += kSelThreads) {
-      const uint32_t key = weight_key(w[i]);
-      if (pass == 0 || (key >> shift[pass - 1]) == prefix) atomicAdd(&hist[(key >> shift[pass]) & (nb - 1)], 1);
-    }
-    __syncthreads();
-    // suffix sums: thread t owns the bins [nb - per (t + 1), nb - per t), from the top down
-    const int per = nb / kSelThreads;  // 2 or 1
-    int c[2] = {0, 0}, mine = 0;
-    for (int j = 0; j < per; ++j) { c[j] = hist[nb - 1 - (tid * per + j)]; mine += c[j]; }
-    int inc = mine;
+  const int per = (old + CS - 1) / CS, lo = min(rank * per, old), hi = min(lo + per, old);
+  const float* w = p.weight + (size_t)unit * p.L;
+  // The slice in chunks of kpt keys per thread.
+  const int kpt = min(kKeys, (hi - lo + kSelThreads - 1) / kSelThreads);
+  const int span = max(kpt, 1) * kSelThreads;
+  const int nchunks = (hi - lo + span - 1) / span;
+  uint32_t key[kKeys];
+  int have = 0;  // keys of the chunk that this thread holds
+  auto load = [&](int chunk) {
+    const int i0 = lo + chunk * span + tid * kpt;
+    have = max(0, min(kpt, hi - i0));
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += u;
+    for (int j = 0; j < kKeys; ++j) key[j] = j < have ? __float_as_uint(w[i0 + j]) : 0u;
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) key[j] = weight_key(__uint_as_float(key[j]));
+  };
+  if (nchunks == 1) load(0);
+  if (tid < 2) share[tid] = 0;
+  for (int i = tid; i < 4 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
+  __syncthreads();
+
+  uint32_t prefix = 0, need = (uint32_t)want;
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), nb = pass == 2 ? 1024 : 2048;
+    for (int c = 0; c < nchunks; ++c) {
+      if (nchunks > 1) load(c);
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j) {
+        const bool in = j < have && (pass == 0 || (key[j] >> (pass == 1 ? 21 : 10)) == prefix);
+        if (in) atomicAdd(&hist[tid & 3][(key[j] >> shift) & (nb - 1)], 1u);
+      }
     }
-    if (lane == 31) wsum[warp] = inc;
     __syncthreads();
-    int before = inc - mine;
-    for (int q = 0; q < warp; ++q) before += wsum[q];
-    for (int j = 0; j < per; ++j) {
-      if (before < need && before + c[j] >= need) {
-        sh_digit = nb - 1 - (tid * per + j);
+    uint32_t* mine = fold[pass & 1];
+    for (int i = tid; i < nb; i += kSelThreads) {
+      mine[i] = hist[0][i] + hist[1][i] + hist[2][i] + hist[3][i];
+      hist[0][i] = hist[1][i] = hist[2][i] = hist[3][i] = 0;
+    }
+    if (CS == 1) __syncthreads(); else cluster.sync();
+    // thread t owns the bins [nb - per (t + 1), nb - per t): an exclusive sum from the top bin down
+    const int pb = nb / kSelThreads;
+    uint32_t c2[2] = {0, 0}, own[2] = {0, 0};
+    for (int j = 0; j < pb; ++j) {
+      const int bin = nb - 1 - (tid * pb + j);
+      own[j] = mine[bin];
+      if (CS == 1) {
+        c2[j] = own[j];
+      } else {
+#pragma unroll
+        for (int q = 0; q < CS; ++q) c2[j] += cluster.map_shared_rank(mine, q)[bin];
+      }
+    }
+    uint32_t total;
+    uint32_t before = block_scan(c2[0] + c2[1], wsum, &total);
+    for (int j = 0; j < pb; ++j) {
+      if (before < need && before + c2[j] >= need) {
+        sh_digit = (uint32_t)(nb - 1 - (tid * pb + j));
         sh_above = before;
       }
-      before += c[j];
+      before += c2[j];
     }
     __syncthreads();
-    prefix = (prefix << bits[pass]) | (uint32_t)sh_digit;
+    const uint32_t digit = sh_digit;
+    uint32_t above = 0;
+    for (int j = 0; j < pb; ++j) {
+      const uint32_t bin = (uint32_t)(nb - 1 - (tid * pb + j));
+      if (bin > digit) above += own[j];
+      if (pass == 2 && bin == digit) share[1] = own[j];
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    if ((tid & 31) == 0 && above != 0) atomicAdd(&share[0], above);
+    prefix = pass == 0 ? digit : (prefix << (pass == 1 ? 11 : 10)) | digit;
     need -= sh_above;
-    __syncthreads();
+    __syncthreads();  // sh_digit, sh_above are written again in the next pass
   }
-  // key > prefix: kept; key == prefix: the first `need` of them.  4096 rows at a time, in order.
-  int gt_done = 0, eq_done = 0;
-  for (int base = 0; base < old; base += 4 * kSelThreads) {
-    uint32_t key[4];
-    uint32_t pk = 0;  // (greater << 16) | equal, over this thread's four rows
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = base + tid * 4 + j;
-      key[j] = i < old ? weight_key(w[i]) : 0u;
-      if (i < old) pk += key[j] > prefix ? 65536u : (key[j] == prefix ? 1u : 0u);
+  // key > prefix: kept; key == prefix: the first `need` of them over the whole head.
+  uint32_t gt = 0, eq = 0;
+  if (CS > 1) {
+    cluster.sync();
+    for (int q = 0; q < rank; ++q) {
+      const uint32_t* o = cluster.map_shared_rank(share, q);
+      gt += o[0];
+      eq += o[1];
     }
-    uint32_t inc = pk;
+  }
+  for (int c = 0; c < nchunks; ++c) {
+    if (nchunks > 1) load(c);
+    uint32_t pk = 0;  // (greater << 16) | equal of this thread's keys: a chunk has 16384 at most
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += u;
-    }
-    if (lane == 31) wsum[warp] = (int)inc;
-    __syncthreads();
-    uint32_t before = inc - pk, all = 0;
-    for (int q = 0; q < kSelThreads / 32; ++q) {
-      const uint32_t v = (uint32_t)wsum[q];
-      if (q < warp) before += v;
-      all += v;
-    }
-    int gt = gt_done + (int)(before >> 16), eq = eq_done + (int)(before & 0xFFFFu);
+    for (int j = 0; j < kKeys; ++j)
+      if (j < have) pk += key[j] > prefix ? 65536u : (key[j] == prefix ? 1u : 0u);
+    uint32_t all;
+    const uint32_t before = block_scan(pk, wsum, &all);
+    uint32_t g = gt + (before >> 16), e = eq + (before & 0xFFFFu);
+    const int i0 = lo + c * span + tid * kpt;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = base + tid * 4 + j;
-      if (i >= old) break;
+    for (int j = 0; j < kKeys; ++j) {
+      if (j >= have) break;
       if (key[j] > prefix) {
-        out[gt + min(eq, need)] = i;
-        ++gt;
+        out[g + min(e, need)] = i0 + j;
+        ++g;
       } else if (key[j] == prefix) {
-        if (eq < need) out[gt + eq] = i;
-        ++eq;
+        if (e < need) out[g + e] = i0 + j;
+        ++e;
       }
     }
-    gt_done += (int)(all >> 16);
-    eq_done += (int)(all & 0xFFFFu);
-    __syncthreads();
+    gt += all >> 16;
+    eq += all & 0xFFFFu;
   }
+  if (CS > 1) cluster.sync();  // the other CTAs have read this one's shared memory
+}
+
+template <int CS>
+static cudaError_t launch_select(const Cache8Evict& p, cudaStream_t st) {
+  constexpr size_t smem = 4 * kBins * sizeof(uint32_t);
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<CS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * CS));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = CS;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = CS > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<CS>, p);
 }
 
 // evict, move: a CTA per (dst block, (b, KV head), K or V).  e4m3 magnitudes order like their 7-bit
@@ -284,22 +367,52 @@ __global__ void __launch_bounds__(kThreads) evict_move_kernel(Cache8Evict p, int
 }
 
 // ---------------------------------------------------------------------------
-// gather: a thread per (token, pair of adjacent output columns)
+// gather: a CTA per 128 tokens of one (b, KV head).  The dominant dims touch nearly every 32-byte
+// sector of a row, so whole rows are read, 16 bytes a lane, and staged in shared memory (row stride
+// D + 4 bytes: the byte reads of neighbouring tokens fall into different banks); the output leaves
+// four bytes (two columns) a thread, contiguous over the CTA's tokens.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ Cache8Gather p) {
-  const size_t items = (size_t)p.B * p.Hkv * p.npos * p.nfc;  // bf16 pairs
-  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < items; i += (size_t)gridDim.x * kThreads) {
-    const int c = (int)(i % p.nfc) * 2;  // column pair (c, c + 1); nfc is even, so both lie in one half
-    size_t r = i / p.nfc;
-    const int t = p.pos0 + (int)(r % p.npos);
-    const size_t unit = r / p.npos;
-    const int g = (int)(unit % p.Hkv);
-    const int hi = c >= p.nfc ? p.D / 2 : 0, cc = c >= p.nfc ? c - p.nfc : c;
-    const uint8_t* row = p.k + (unit * p.L + t) * p.D + hi;
-    const uint32_t a = row[p.fc[g * p.nfc + cc]], d = row[p.fc[g * p.nfc + cc + 1]];
-    const float f = p.ks[unit * p.nblk + t / p.T];
-    const float2 v = __half22float2(from_e4m3x2(a | (d << 8)));
-    reinterpret_cast<uint32_t*>(p.out)[(unit * p.L + t) * p.nfc + c / 2] = pack_bf16x2(v.x * f, v.y * f);
+constexpr int kGatherTokens = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ Cache8Gather p, int tiles) {
+  constexpr int STRIDE = D + 4, CPR = D / 16;
+  __shared__ uint32_t rows[kGatherTokens * STRIDE / 4];
+  __shared__ float sc[kGatherTokens];
+  __shared__ uint16_t pair[128];  // byte offsets of the two dims of an output word
+  const int tid = threadIdx.x;
+  const int unit = blockIdx.x / tiles, g = unit % p.Hkv;
+  const int t0 = p.pos0 + (blockIdx.x % tiles) * kGatherTokens;
+  const int n = min(kGatherTokens, p.pos0 + p.npos - t0);
+  const uint4* src = reinterpret_cast<const uint4*>(p.k + ((size_t)unit * p.L + t0) * D);
+#pragma unroll
+  for (int i = 0; i < kGatherTokens * CPR / kThreads; ++i) {
+    const int c = tid + i * kThreads, r = c / CPR;
+    if (r < n) {
+      const uint4 u = __ldg(src + c);
+      uint32_t* d = rows + r * (STRIDE / 4) + (c % CPR) * 4;
+      d[0] = u.x; d[1] = u.y; d[2] = u.z; d[3] = u.w;
+    }
+  }
+  if (tid < n) sc[tid] = __ldg(p.ks + (size_t)unit * p.nblk + (t0 + tid) / p.T);
+  for (int w = tid; w < p.nfc; w += kThreads) {  // word w: columns 2 w and 2 w + 1 (nfc is even: one half)
+    const int hi = 2 * w >= p.nfc, c = 2 * w - (hi ? p.nfc : 0);
+    const uint8_t* f = p.fc + g * p.nfc + c;
+    pair[w] = (uint16_t)((f[0] + (hi ? D / 2 : 0)) | ((f[1] + (hi ? D / 2 : 0)) << 8));
+  }
+  __syncthreads();
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.out) + ((size_t)unit * p.L + t0) * p.nfc;
+  const int step_r = kThreads / p.nfc, step_w = kThreads % p.nfc;
+  int r = tid / p.nfc, w = tid % p.nfc;
+  const uint8_t* bytes = reinterpret_cast<const uint8_t*>(rows);
+  for (int i = tid; i < n * p.nfc; i += kThreads) {
+    const uint32_t at = pair[w];
+    const uint8_t* row = bytes + r * STRIDE;
+    const float2 v = __half22float2(from_e4m3x2(row[at & 255u] | ((uint32_t)row[at >> 8] << 8)));
+    out[i] = pack_bf16x2(v.x * sc[r], v.y * sc[r]);
+    r += step_r;
+    w += step_w;
+    if (w >= p.nfc) { w -= p.nfc; ++r; }
   }
 }
 
@@ -326,8 +439,9 @@ cudaError_t launch_cache8_append(const Cache8Append& p, cudaStream_t st) {
 }
 
 cudaError_t launch_cache8_evict(const Cache8Evict& p, cudaStream_t st) {
-  evict_select_kernel<<<p.B * p.Hkv, kSelThreads, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+  if ((long long)p.B * p.Hkv * 8 >= (1LL << 31)) return cudaErrorInvalidValue;
+  // Slices of about a register-full (16384 keys) or less, at least 4096.
+  cudaError_t e = p.L > 16384 ? launch_select<8>(p, st) : (p.L > 4096 ? launch_select<2>(p, st) : launch_select<1>(p, st));
   if (e != cudaSuccess) return e;
   const int most = p.keep < p.L ? p.keep : p.L;
   const int nb = (most + p.T - 1) / p.T;
@@ -345,11 +459,11 @@ cudaError_t launch_cache8_evict(const Cache8Evict& p, cudaStream_t st) {
 }
 
 cudaError_t launch_cache8_gather(const Cache8Gather& p, cudaStream_t st) {
-  const size_t items = (size_t)p.B * p.Hkv * p.npos * p.nfc;
-  if (items == 0) return cudaSuccess;
-  size_t blocks = (items + kThreads - 1) / kThreads;
-  if (blocks > (size_t)148 * 32) blocks = (size_t)148 * 32;
-  gather_kernel<<<(unsigned)blocks, kThreads, 0, st>>>(p);
+  if (p.npos == 0) return cudaSuccess;
+  const int tiles = (p.npos + kGatherTokens - 1) / kGatherTokens;
+  const unsigned grid = (unsigned)tiles * p.B * p.Hkv;
+  if (p.D == 128) gather_kernel<128><<<grid, kThreads, 0, st>>>(p, tiles);
+  else gather_kernel<64><<<grid, kThreads, 0, st>>>(p, tiles);
   return cudaGetLastError();
 }
 

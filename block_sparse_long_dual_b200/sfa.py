@@ -687,6 +687,25 @@ class FasaDecode:
 # ---------------------------------------------------------------------------
 # 8-bit KV cache: e4m3 codes with a power-of-two scale per block of tokens and head
 # ---------------------------------------------------------------------------
+def _fits(t, name, shape, dtype, device):
+    """Address of a buffer that _expect accepts (None: NULL).  The common case is tested here in one go (a decode
+    step's calls are a few microseconds of GPU work each); anything else goes through _expect, which names what
+    is wrong.  ``device`` is the current device (_here)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        _expect(t, name, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _here(cache):
+    """The cache's device, which must be the current one."""
+    dev = cache.k.device
+    if dev.index != torch.cuda.current_device():
+        _cuda(cache.k, "the cache")
+    return dev
+
+
 class KvCache8:
     """Keys and values of ``B`` sequences in 8 bits (sfa_cache8 of include/sfa.h).
 
@@ -714,6 +733,7 @@ class KvCache8:
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._c = Cache8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), lens.data_ptr(),
                          None if weight is None else weight.data_ptr(), block)
+        self._cref = ctypes.byref(self._c)
         self._shapes = {}
         self._workspaces = {}
 
@@ -734,6 +754,12 @@ class KvCache8:
         if s is None:
             s = self._shapes[heads_q] = Shape(self.batch, heads_q, self.heads_kv, self.capacity, self.head_dim, BF16)
         return s
+
+    def _status_ptr(self, status):
+        if status is self.status:
+            return status.data_ptr()
+        _status(status)
+        return None if status is None else status.data_ptr()
 
     def _workspace(self, q, weights):
         """The handle's own attention workspace for queries like q (one per shape, made on first use)."""
@@ -773,15 +799,13 @@ def cache8_append(cache: KvCache8, K, V, *, at=None, counts=None, status=None, s
     if K.dim() != 4:
         raise ValueError("K must be [B, Hkv, n, d]")
     n = K.shape[2]
-    dev = cache.k.device
-    rows = (cache.batch, cache.heads_kv, n, cache.head_dim)
-    _expect(K, "K", rows, torch.bfloat16, dev)
-    _expect(V, "V", rows, torch.bfloat16, dev)
-    _expect(at, "at", (cache.batch,), torch.int32, dev)
-    _expect(counts, "counts", (cache.batch,), torch.int32, dev)
-    _status(status)
-    _check(lib.sfa_cache8_append(ctypes.byref(cache.shape(cache.heads_kv)), ctypes.byref(cache._c), _ptr(K), _ptr(V),
-                                 n, _ptr(at), _ptr(counts), _ptr(status), _stream(stream)), "sfa_cache8_append")
+    dev = _here(cache)
+    rows, seqs = (cache.batch, cache.heads_kv, n, cache.head_dim), (cache.batch,)
+    _check(lib.sfa_cache8_append(ctypes.byref(cache.shape(cache.heads_kv)), cache._cref,
+                                 _fits(K, "K", rows, torch.bfloat16, dev), _fits(V, "V", rows, torch.bfloat16, dev), n,
+                                 _fits(at, "at", seqs, torch.int32, dev),
+                                 _fits(counts, "counts", seqs, torch.int32, dev), cache._status_ptr(status),
+                                 _stream(stream)), "sfa_cache8_append")
 
 
 def _cache8_query(q, cache: KvCache8):
@@ -806,22 +830,20 @@ def cache8_attn(q, cache: KvCache8, *, back: int = 0, scale: float = 0.0, o=None
     cache; returns o.  With ``weight_out`` every token's attention weight is added to ``weight_in``."""
     lib = load()
     shape, nq = _cache8_query(q, cache)
-    dev = cache.k.device
-    _expect(q, "q", q.shape, torch.bfloat16, dev)
+    dev = _here(cache)
     o = torch.empty_like(q) if o is None else o
-    _expect(o, "o", q.shape, torch.bfloat16, dev)
-    _expect(lse, "lse", q.shape[:-1], torch.float32, dev)
     tokens = (cache.batch, cache.heads_kv, cache.capacity)
-    _expect(weight_in, "weight_in", tokens, torch.float32, dev)
-    _expect(weight_out, "weight_out", tokens, torch.float32, dev)
     if workspace is None:
         workspace = torch.empty(cache8_attn_workspace(q, cache, weights=weight_out is not None), dtype=torch.uint8,
                                 device=dev)
-    _workspace(workspace)
-    _status(status)
-    _check(lib.sfa_cache8_attn(ctypes.byref(shape), ctypes.byref(cache._c), _ptr(q), nq, int(back), float(scale),
-                               _ptr(o), _ptr(lse), _ptr(weight_in), _ptr(weight_out), _ptr(workspace),
-                               workspace.numel(), _ptr(status), _stream(stream)), "sfa_cache8_attn")
+    nbytes = workspace.numel()
+    _check(lib.sfa_cache8_attn(ctypes.byref(shape), cache._cref, _fits(q, "q", q.shape, torch.bfloat16, dev), nq,
+                               back, scale, _fits(o, "o", q.shape, torch.bfloat16, dev),
+                               _fits(lse, "lse", q.shape[:-1], torch.float32, dev),
+                               _fits(weight_in, "weight_in", tokens, torch.float32, dev),
+                               _fits(weight_out, "weight_out", tokens, torch.float32, dev),
+                               _fits(workspace, "workspace", (nbytes,), torch.uint8, dev), nbytes,
+                               cache._status_ptr(status), _stream(stream)), "sfa_cache8_attn")
     return o
 
 
@@ -831,16 +853,14 @@ def cache8_attn_list(q, cache: KvCache8, idx, *, scale: float = 0.0, o=None, lse
     if q.dim() != 3 or idx.dim() != 3:
         raise ValueError("q must be [B, Hq, d] and idx [B, Hq, k]")
     shape, _ = _cache8_query(q, cache)
-    dev = cache.k.device
-    _expect(q, "q", q.shape, torch.bfloat16, dev)
+    dev = _here(cache)
     o = torch.empty_like(q) if o is None else o
-    _expect(o, "o", q.shape, torch.bfloat16, dev)
-    _expect(idx, "idx", (*q.shape[:2], idx.shape[-1]), torch.int32, dev)
-    _expect(lse, "lse", q.shape[:2], torch.float32, dev)
-    _status(status)
-    _check(lib.sfa_cache8_attn_list(ctypes.byref(shape), ctypes.byref(cache._c), _ptr(q), _ptr(idx), idx.shape[-1],
-                                    float(scale), _ptr(o), _ptr(lse), _ptr(status), _stream(stream)),
-           "sfa_cache8_attn_list")
+    rows, k = q.shape[:2], idx.shape[2]
+    _check(lib.sfa_cache8_attn_list(ctypes.byref(shape), cache._cref, _fits(q, "q", q.shape, torch.bfloat16, dev),
+                                    _fits(idx, "idx", (*rows, k), torch.int32, dev), k, scale,
+                                    _fits(o, "o", q.shape, torch.bfloat16, dev),
+                                    _fits(lse, "lse", rows, torch.float32, dev), cache._status_ptr(status),
+                                    _stream(stream)), "sfa_cache8_attn_list")
     return o
 
 
@@ -857,36 +877,36 @@ def cache8_evict(src: KvCache8, dst: KvCache8, *, keep: int, recent: int = 0, id
     """sfa_cache8_evict: the last ``recent`` tokens and those of the largest ``src.weight``, ``keep`` in all,
     move to ``dst``; returns idx [B, Hkv, keep] int32, their rows in src (ascending, -1 padded)."""
     lib = load()
-    dev = src.k.device
+    dev = _here(src)
     if (dst.batch, dst.heads_kv, dst.head_dim) != (src.batch, src.heads_kv, src.head_dim):
         raise ValueError("dst must have the batch, heads and head dim of src")
     if dst.k.device != dev:
         raise ValueError(f"dst must be on {dev}, got {dst.k.device}")
     if idx is None:
         idx = torch.empty((src.batch, src.heads_kv, max(int(keep), 0)), dtype=torch.int32, device=dev)
-    _expect(idx, "idx", (src.batch, src.heads_kv, keep), torch.int32, dev)
-    if workspace is not None:
-        _workspace(workspace)
-    _status(status)
-    _check(lib.sfa_cache8_evict(ctypes.byref(src.shape(src.heads_kv)), ctypes.byref(src._c), ctypes.byref(dst._c),
-                                dst.capacity, int(keep), int(recent), _ptr(idx), _ptr(workspace),
-                                0 if workspace is None else workspace.numel(), _ptr(status), _stream(stream)),
-           "sfa_cache8_evict")
+    nbytes = 0 if workspace is None else workspace.numel()
+    _check(lib.sfa_cache8_evict(ctypes.byref(src.shape(src.heads_kv)), src._cref, dst._cref, dst.capacity, keep, recent,
+                                _fits(idx, "idx", (src.batch, src.heads_kv, keep), torch.int32, dev),
+                                _fits(workspace, "workspace", (nbytes,), torch.uint8, dev), nbytes,
+                                src._status_ptr(status), _stream(stream)), "sfa_cache8_evict")
     return idx
 
 
 def cache8_fc_gather(cache: KvCache8, fc, *, K_fc=None, pos0: int = 0, npos: int | None = None, stream=None):
     """sfa_cache8_fc_gather: the compact dominant-pair copy K_fc [B, Hkv, capacity, 2 nfc] bf16 of the cached keys."""
+    import numpy as np
     lib = load()
-    fch, nfc = _fc_host(fc)
+    pairs = np.ascontiguousarray(fc, dtype=np.int32)
+    if pairs.ndim != 2 or pairs.shape[0] != cache.heads_kv:
+        raise ValueError("fc must be [heads_kv, nfc]")
+    nfc = pairs.shape[1]
+    dev = _here(cache)
     rows = (cache.batch, cache.heads_kv, cache.capacity, 2 * nfc)
-    if len(fch) != cache.heads_kv * nfc:
-        raise ValueError("fc must have a row per KV head")
-    K_fc = torch.empty(rows, dtype=torch.bfloat16, device=cache.k.device) if K_fc is None else K_fc
-    _expect(K_fc, "K_fc", rows, torch.bfloat16, cache.k.device)
+    K_fc = torch.empty(rows, dtype=torch.bfloat16, device=dev) if K_fc is None else K_fc
     npos = cache.capacity - pos0 if npos is None else npos
-    _check(lib.sfa_cache8_fc_gather(ctypes.byref(cache.shape(cache.heads_kv)), ctypes.byref(cache._c), fch, nfc, pos0,
-                                    npos, _ptr(K_fc), _stream(stream)), "sfa_cache8_fc_gather")
+    _check(lib.sfa_cache8_fc_gather(ctypes.byref(cache.shape(cache.heads_kv)), cache._cref, pairs.ctypes.data, nfc, pos0,
+                                    npos, _fits(K_fc, "K_fc", rows, torch.bfloat16, dev), _stream(stream)),
+           "sfa_cache8_fc_gather")
     return K_fc
 
 
