@@ -116,20 +116,28 @@ __global__ void advance_kernel(Cache8Append p) {
 // ---------------------------------------------------------------------------
 // evict, selection: a cluster of CS CTAs per (b, KV head), each over a contiguous
 // slice of the tokens.  Radix select (11 + 11 + 10 bits) of the order-preserving
-// weight keys: the slices' histograms are summed through distributed shared
-// memory, so every CTA finds the same threshold; a slice's own histograms also
-// tell how many kept rows lie before the next one.  A thread holds up to kKeys
-// consecutive keys in registers through all passes (a longer slice is read again
-// in each pass), so the kept rows leave in order after one scan.
-// Accumulated weights share few leading bits, so neighbouring lanes would queue on
-// one bin: four copies of the histogram, one per lane mod 4.
+// weight keys.  The slices' histograms are summed through distributed shared
+// memory, each CTA an eighth of the bins; every CTA then finds the eighth and the
+// bin of the threshold.  A slice's own histogram also tells how many kept rows lie
+// before the next slice's.  The slice's keys stay in shared memory through all
+// passes (a longer slice is read again in each pass) and the loops over them are
+// short code: keys in registers meant every loop unrolled, run once or three
+// times, and waiting for instructions.  Accumulated weights share few leading
+// bits, so neighbouring lanes would queue on one bin: two copies of the histogram,
+// sixteen banks apart.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
-constexpr int kKeys = 16;
-constexpr int kBins = 2048;
+constexpr int kSlice = 16384;  // keys in shared memory
+constexpr int kBins = 2048, kBinStride = kBins + 16;
+constexpr int kBpt = kBins / kSelThreads;  // bins per thread
+constexpr int kPerThread = kSlice / kSelThreads;
+// One word of padding per thread's 16 consecutive keys: both orders of access spread over the banks.
+__device__ __forceinline__ int key_at(int i) { return i + i / kPerThread; }
+constexpr int kKeyWords = kSlice + kSelThreads;
+constexpr size_t kSelSmem = ((size_t)kKeyWords + 2 * kBinStride) * sizeof(uint32_t);
 
-// Exclusive sum over the block of a 32-bit value, and the total.
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* wsum, uint32_t* total) {
+// Exclusive sum over the block of a 32-bit value.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* wsum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t inc = x;
 #pragma unroll
@@ -140,22 +148,22 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* wsum, uint3
   __syncthreads();  // wsum may still be read from the call before
   if (lane == 31) wsum[warp] = inc;
   __syncthreads();
-  const uint32_t w = wsum[lane];
-  *total = __reduce_add_sync(0xffffffffu, w);
-  return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u) + inc - x;
+  return __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0u) + inc - x;
 }
 
 template <int CS>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ Cache8Evict p) {
-  extern __shared__ uint32_t hist_raw[];
-  uint32_t (*hist)[kBins] = reinterpret_cast<uint32_t (*)[kBins]>(hist_raw);  // [4][kBins]
-  __shared__ uint32_t fold[2][kBins];
-  __shared__ uint32_t wsum[32];
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __grid_constant__ Cache8Evict p) {
+  extern __shared__ __align__(16) uint32_t sel_smem[];
+  uint32_t* key = sel_smem;                // [kKeyWords], through key_at
+  uint32_t* hist = sel_smem + kKeyWords;   // [2][kBinStride]
+  __shared__ uint32_t fold[2][CS > 1 ? kBins : 1];  // this slice's bins (two: a pass may begin while others read)
+  __shared__ uint32_t part[2][CS > 1 ? kBins / CS : 1], ptotal[2];  // this CTA's share of the bins, over all slices
+  __shared__ uint32_t wsum[kSelThreads / 32];
   __shared__ uint32_t share[2];  // this slice's keys above and at the threshold
   __shared__ uint32_t sh_digit, sh_above;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = CS == 1 ? 0 : (int)cluster.block_rank();
-  const int unit = blockIdx.x / CS, b = unit / p.Hkv, tid = threadIdx.x;
+  const int unit = blockIdx.x / CS, b = unit / p.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int n = p.lens[b];
   if (n < 0 || n > p.L) {
     if (tid == 0) report(p.status, SFA_ERR_INDEX);
@@ -173,76 +181,103 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
 
   const int per = (old + CS - 1) / CS, lo = min(rank * per, old), hi = min(lo + per, old);
   const float* w = p.weight + (size_t)unit * p.L;
-  // The slice in chunks of kpt keys per thread.
-  const int kpt = min(kKeys, (hi - lo + kSelThreads - 1) / kSelThreads);
-  const int span = max(kpt, 1) * kSelThreads;
-  const int nchunks = (hi - lo + span - 1) / span;
-  uint32_t key[kKeys];
-  int have = 0;  // keys of the chunk that this thread holds
-  auto load = [&](int chunk) {
-    const int i0 = lo + chunk * span + tid * kpt;
-    have = max(0, min(kpt, hi - i0));
-#pragma unroll
-    for (int j = 0; j < kKeys; ++j) key[j] = j < have ? __float_as_uint(w[i0 + j]) : 0u;
-#pragma unroll
-    for (int j = 0; j < kKeys; ++j) key[j] = weight_key(__uint_as_float(key[j]));
+  int first = lo, cnt = 0;  // the keys in shared memory: rows [first, first + cnt)
+  auto load = [&](int from) {
+    __syncthreads();  // everyone is done with the keys before
+    first = from;
+    cnt = min(kSlice, hi - from);
+#pragma unroll 8
+    for (int i = tid; i < cnt; i += kSelThreads) key[key_at(i)] = weight_key(__ldg(w + from + i));
+    __syncthreads();
   };
-  if (nchunks == 1) load(0);
+  const bool whole = hi - lo <= kSlice;
   if (tid < 2) share[tid] = 0;
-  for (int i = tid; i < 4 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
-  __syncthreads();
+  for (int i = tid; i < 2 * kBinStride; i += kSelThreads) hist[i] = 0;
+  if (whole) load(lo);
+  else __syncthreads();
 
   uint32_t prefix = 0, need = (uint32_t)want;
-#pragma unroll
+#pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), nb = pass == 2 ? 1024 : 2048;
-    for (int c = 0; c < nchunks; ++c) {
-      if (nchunks > 1) load(c);
-#pragma unroll
-      for (int j = 0; j < kKeys; ++j) {
-        const bool in = j < have && (pass == 0 || (key[j] >> (pass == 1 ? 21 : 10)) == prefix);
-        if (in) atomicAdd(&hist[tid & 3][(key[j] >> shift) & (nb - 1)], 1u);
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), up = pass == 1 ? 21 : 10;
+    const uint32_t mask = pass == 2 ? 1023u : 2047u;  // (the last pass leaves the upper bins empty)
+    uint32_t* copy = hist + (lane & 1) * kBinStride;
+    for (int from = lo; from < hi; from += kSlice) {
+      if (!whole) load(from);
+#pragma unroll 4
+      for (int i = tid; i < cnt; i += kSelThreads) {
+        const uint32_t k = key[key_at(i)];
+        if (pass == 0 || (k >> up) == prefix) atomicAdd(copy + ((k >> shift) & mask), 1u);
       }
     }
     __syncthreads();
-    uint32_t* mine = fold[pass & 1];
-    for (int i = tid; i < nb; i += kSelThreads) {
-      mine[i] = hist[0][i] + hist[1][i] + hist[2][i] + hist[3][i];
-      hist[0][i] = hist[1][i] = hist[2][i] = hist[3][i] = 0;
-    }
-    if (CS == 1) __syncthreads(); else cluster.sync();
-    // thread t owns the bins [nb - per (t + 1), nb - per t): an exclusive sum from the top bin down
-    const int pb = nb / kSelThreads;
-    uint32_t c2[2] = {0, 0}, own[2] = {0, 0};
-    for (int j = 0; j < pb; ++j) {
-      const int bin = nb - 1 - (tid * pb + j);
-      own[j] = mine[bin];
-      if (CS == 1) {
-        c2[j] = own[j];
-      } else {
+    // Thread t owns the bins [2 t', 2 t' + 2), t' = 1023 - t: an exclusive sum over t runs from the top bin down.
+    const int bin0 = kBins - kBpt * (tid + 1);
+    uint32_t own[kBpt] = {0, 0};
 #pragma unroll
-        for (int q = 0; q < CS; ++q) c2[j] += cluster.map_shared_rank(mine, q)[bin];
-      }
+    for (int q = 0; q < 2; ++q) {
+      uint2* h = reinterpret_cast<uint2*>(hist + q * kBinStride + bin0);
+      const uint2 u = *h;
+      own[0] += u.x;
+      own[1] += u.y;
+      *h = make_uint2(0, 0);
     }
-    uint32_t total;
-    uint32_t before = block_scan(c2[0] + c2[1], wsum, &total);
-    for (int j = 0; j < pb; ++j) {
-      if (before < need && before + c2[j] >= need) {
-        sh_digit = (uint32_t)(nb - 1 - (tid * pb + j));
+    if (CS > 1) {
+      constexpr int PB = kBins / CS;
+      uint32_t *mine = fold[pass & 1], *sum = part[pass & 1];
+      *reinterpret_cast<uint2*>(mine + bin0) = make_uint2(own[0], own[1]);
+      if (tid == 0) ptotal[pass & 1] = 0;
+      cluster.sync();
+      if (tid < PB) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int q = 0; q < CS; ++q) v += cluster.map_shared_rank(mine, q)[rank * PB + tid];
+        sum[tid] = v;
+        v = __reduce_add_sync(0xffffffffu, v);
+        if (lane == 0 && v != 0) atomicAdd(&ptotal[pass & 1], v);
+      }
+      cluster.sync();
+      // The eighth that holds the threshold (from the top down), and the keys above it.
+      const uint32_t t = lane < CS ? *cluster.map_shared_rank(&ptotal[pass & 1], CS - 1 - lane) : 0u;
+      uint32_t run = 0, skipped = 0;
+      int e = -1;
+#pragma unroll
+      for (int q = 0; q < CS; ++q) {
+        const uint32_t v = __shfl_sync(0xffffffffu, t, q);
+        if (e < 0 && run + v >= need) {
+          e = CS - 1 - q;
+          skipped = run;
+        }
+        run += v;
+      }
+      const uint32_t v = tid < PB ? cluster.map_shared_rank(sum, e)[PB - 1 - tid] : 0u;
+      const uint32_t before = skipped + block_scan(v, wsum);
+      if (tid < PB && before < need && before + v >= need) {
+        sh_digit = (uint32_t)(e * PB + PB - 1 - tid);
         sh_above = before;
       }
-      before += c2[j];
+    } else {
+      uint32_t before = block_scan(own[0] + own[1], wsum);
+#pragma unroll
+      for (int j = kBpt - 1; j >= 0; --j) {
+        if (before < need && before + own[j] >= need) {
+          sh_digit = (uint32_t)(bin0 + j);
+          sh_above = before;
+        }
+        before += own[j];
+      }
     }
     __syncthreads();
     const uint32_t digit = sh_digit;
     uint32_t above = 0;
-    for (int j = 0; j < pb; ++j) {
-      const uint32_t bin = (uint32_t)(nb - 1 - (tid * pb + j));
+#pragma unroll
+    for (int j = 0; j < kBpt; ++j) {
+      const uint32_t bin = (uint32_t)(bin0 + j);
       if (bin > digit) above += own[j];
       if (pass == 2 && bin == digit) share[1] = own[j];
     }
     above = __reduce_add_sync(0xffffffffu, above);
-    if ((tid & 31) == 0 && above != 0) atomicAdd(&share[0], above);
+    if (lane == 0 && above != 0) atomicAdd(&share[0], above);
     prefix = pass == 0 ? digit : (prefix << (pass == 1 ? 11 : 10)) | digit;
     need -= sh_above;
     __syncthreads();  // sh_digit, sh_above are written again in the next pass
@@ -257,40 +292,42 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
       eq += o[1];
     }
   }
-  for (int c = 0; c < nchunks; ++c) {
-    if (nchunks > 1) load(c);
-    uint32_t pk = 0;  // (greater << 16) | equal of this thread's keys: a chunk has 16384 at most
-#pragma unroll
-    for (int j = 0; j < kKeys; ++j)
-      if (j < have) pk += key[j] > prefix ? 65536u : (key[j] == prefix ? 1u : 0u);
-    uint32_t all;
-    const uint32_t before = block_scan(pk, wsum, &all);
+  for (int from = lo; from < hi; from += kSlice) {
+    if (!whole) load(from);
+    const uint32_t* mine = key + tid * (kPerThread + 1);  // the keys [16 tid, 16 tid + 16)
+    const int have = min(kPerThread, cnt - tid * kPerThread);
+    uint32_t pk = 0;  // (greater << 16) | equal: 16384 keys at most
+#pragma unroll 4
+    for (int j = 0; j < have; ++j) pk += mine[j] > prefix ? 65536u : (mine[j] == prefix ? 1u : 0u);
+    const uint32_t before = block_scan(pk, wsum);
     uint32_t g = gt + (before >> 16), e = eq + (before & 0xFFFFu);
-    const int i0 = lo + c * span + tid * kpt;
-#pragma unroll
-    for (int j = 0; j < kKeys; ++j) {
-      if (j >= have) break;
-      if (key[j] > prefix) {
-        out[g + min(e, need)] = i0 + j;
-        ++g;
-      } else if (key[j] == prefix) {
-        if (e < need) out[g + e] = i0 + j;
-        ++e;
+    if (pk != 0) {
+#pragma unroll 4
+      for (int j = 0; j < have; ++j) {
+        const uint32_t k = mine[j];
+        if (k >= prefix) {
+          if (k > prefix || e < need) out[g + min(e, need)] = first + tid * kPerThread + j;
+          g += k > prefix;
+          e += k == prefix;
+        }
       }
     }
-    gt += all >> 16;
-    eq += all & 0xFFFFu;
+    if (!whole) {  // wsum still holds the warps' totals
+      const uint32_t all = __reduce_add_sync(0xffffffffu, wsum[lane]);
+      gt += all >> 16;
+      eq += all & 0xFFFFu;
+    }
   }
   if (CS > 1) cluster.sync();  // the other CTAs have read this one's shared memory
 }
 
 template <int CS>
 static cudaError_t launch_select(const Cache8Evict& p, cudaStream_t st) {
-  constexpr size_t smem = 4 * kBins * sizeof(uint32_t);
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<CS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<CS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)kSelSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = kSelSmem;
   cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * CS));
   cfg.blockDim = dim3(kSelThreads);
   cfg.stream = st;
@@ -440,8 +477,8 @@ cudaError_t launch_cache8_append(const Cache8Append& p, cudaStream_t st) {
 
 cudaError_t launch_cache8_evict(const Cache8Evict& p, cudaStream_t st) {
   if ((long long)p.B * p.Hkv * 8 >= (1LL << 31)) return cudaErrorInvalidValue;
-  // Slices of about a register-full (16384 keys) or less, at least 4096.
-  cudaError_t e = p.L > 16384 ? launch_select<8>(p, st) : (p.L > 4096 ? launch_select<2>(p, st) : launch_select<1>(p, st));
+  // One CTA's shared memory holds 16384 keys; longer caches are spread over eight CTAs a head.
+  cudaError_t e = p.L > kSlice ? launch_select<8>(p, st) : launch_select<1>(p, st);
   if (e != cudaSuccess) return e;
   const int most = p.keep < p.L ? p.keep : p.L;
   const int nb = (most + p.T - 1) / p.T;

@@ -440,6 +440,8 @@ EVICTS = [  # B, Hkv, cap, d, block, keep, recent, dst capacity, lens
     (2, 1, 700, 128, 64, 333, 0, 400, (700, 334)),
     (1, 8, 9000, 128, 128, 1100, 128, 1200, (9000,)),
     (2, 1, 300, 64, 128, 400, 7, 450, (300, 299)),
+    (2, 1, 20000, 64, 64, 1500, 100, 1600, (20000, 17)),     # slices over a cluster of CTAs
+    (1, 1, 140000, 64, 128, 2000, 31, 2000, (139999,)),      # longer than the clusters' registers hold
 ]
 
 
