@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace sfa {
@@ -215,6 +217,21 @@ struct Cache8Gather {
   int B, Hkv, L, D, T, nblk, nfc, pos0, npos;
   uint8_t fc[1024];
 };
+
+// Sets a kernel's dynamic shared memory (and, for kernels that live off it, the largest carve-out) once per device:
+// `done` is the kernel's own word, a bit per device ordinal.  Two threads that race set the same values twice.
+template <typename K>
+inline cudaError_t allow_smem_once(K kern, size_t bytes, bool carveout, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && carveout) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 cudaError_t launch_cache8_append(const Cache8Append& p, cudaStream_t st);
 cudaError_t launch_cache8_evict(const Cache8Evict& p, cudaStream_t st);

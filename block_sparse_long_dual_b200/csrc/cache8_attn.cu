@@ -199,24 +199,24 @@ static cudaError_t launch_join_d(const Cache8Attn& p, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // Index lists: CTA per (b, q head).  A row of d codes is read by d / 16 lanes,
 // 16 bytes each; each such lane group runs its own online softmax over its
-// tokens, kListBatch of them with both loads in flight, and the groups are
-// joined at the end.
+// tokens, BATCH of them with both loads in flight, and the groups are
+// joined at the end.  The list is checked and staged in shared memory first
+// (kListPart entries at a time), so that a row's address waits for no second load.
 // ---------------------------------------------------------------------------
-constexpr int kListBatch = 4;
+constexpr int kListPart = 2048;
 
-template <int D, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) attn_list_kernel(Cache8Attn p) {
+template <int D, int WARPS, int BATCH, int CTAS>
+__global__ void __launch_bounds__(WARPS * 32, CTAS) attn_list_kernel(const __grid_constant__ Cache8Attn p) {
   constexpr int LPT = D / 16, GROUPS = WARPS * 32 / LPT;
+  __shared__ int list[kListPart];
   __shared__ float gm[GROUPS], gl[GROUPS];
-  __shared__ float go[GROUPS][D + 4];
+  __shared__ __align__(16) float go[GROUPS][D + 4];
   __shared__ int bad;
   const int row = blockIdx.x, b = row / p.Hq, h = row % p.Hq, g = h / (p.Hq / p.Hkv);
   const int unit = b * p.Hkv + g;
   const int tid = threadIdx.x, grp = tid / LPT, part = tid % LPT;
-  const int* list = p.idx + (size_t)row * p.k_list;
+  const int* src = p.idx + (size_t)row * p.k_list;
   if (tid == 0) bad = 0;
-  __syncthreads();
-  const int n = visible(p.lens, b, p.L, 0, tid == 0 ? p.status : nullptr);
   float q[16];
   {
     const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (size_t)row * D + part * 16);
@@ -231,75 +231,89 @@ __global__ void __launch_bounds__(WARPS * 32) attn_list_kernel(Cache8Attn p) {
       }
     }
   }
+  const int n = visible(p.lens, b, p.L, 0, tid == 0 ? p.status : nullptr);
+  const uint8_t* kbase = p.k + (size_t)unit * p.L * D + part * 16;
+  const uint8_t* vbase = p.v + (size_t)unit * p.L * D + part * 16;
+  const float* ksp = p.ks + (size_t)unit * p.nblk;
+  const float* vsp = p.vs + (size_t)unit * p.nblk;
+  const int tshift = p.T == 128 ? 7 : 6;
   float m = -INFINITY, l = 0.f, acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-  // the warp's groups walk the list together (a group past the end has no token): the shuffles need all lanes
-  for (int base = 0; base < p.k_list; base += GROUPS * kListBatch) {
-    int tok[kListBatch];
-    uint4 ku[kListBatch], vu[kListBatch];
-    float ks[kListBatch], vs[kListBatch];
-#pragma unroll
-    for (int u = 0; u < kListBatch; ++u) {
-      const int j = base + u * GROUPS + grp;
-      int t = j < p.k_list ? __ldg(list + j) : -1;
+  for (int from = 0; from < p.k_list; from += kListPart) {
+    const int have = min(kListPart, p.k_list - from);
+    __syncthreads();
+    for (int i = tid; i < have; i += WARPS * 32) {
+      int t = __ldg(src + from + i);
       if (t >= n || t < -1) {
         bad = 1;
         t = -1;
       }
-      tok[u] = t;
+      list[i] = t;
     }
+    __syncthreads();
+    // the warp's groups walk the list together (a group past the end has no token): the shuffles need all lanes
+    for (int base = 0; base < have; base += GROUPS * BATCH) {
+      int tok[BATCH];
+      uint4 ku[BATCH], vu[BATCH];
+      float ks[BATCH], vs[BATCH];
 #pragma unroll
-    for (int u = 0; u < kListBatch; ++u) {
-      ku[u] = vu[u] = make_uint4(0, 0, 0, 0);
-      ks[u] = vs[u] = 0.f;
-      if (tok[u] >= 0) {
-        const size_t at = ((size_t)unit * p.L + tok[u]) * D + part * 16;
-        ku[u] = __ldg(reinterpret_cast<const uint4*>(p.k + at));
-        vu[u] = __ldg(reinterpret_cast<const uint4*>(p.v + at));
-        ks[u] = __ldg(p.ks + (size_t)unit * p.nblk + tok[u] / p.T);
-        vs[u] = __ldg(p.vs + (size_t)unit * p.nblk + tok[u] / p.T);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kListBatch; ++u) {
-      const uint32_t kw[4] = {ku[u].x, ku[u].y, ku[u].z, ku[u].w};
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float kv[4];
-        from_e4m3x4(kw[e], kv);
-#pragma unroll
-        for (int z = 0; z < 4; ++z) s = fmaf(q[e * 4 + z], kv[z], s);
+      for (int u = 0; u < BATCH; ++u) {
+        const int j = base + u * GROUPS + grp;
+        tok[u] = j < have ? list[j] : -1;
+        ku[u] = vu[u] = make_uint4(0, 0, 0, 0);
+        ks[u] = vs[u] = 0.f;
+        if (tok[u] >= 0) {
+          const size_t at = (size_t)tok[u] * D;
+          ku[u] = __ldg(reinterpret_cast<const uint4*>(kbase + at));
+          vu[u] = __ldg(reinterpret_cast<const uint4*>(vbase + at));
+          ks[u] = __ldg(ksp + (tok[u] >> tshift));
+          vs[u] = __ldg(vsp + (tok[u] >> tshift));
+        }
       }
 #pragma unroll
-      for (int o = LPT / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (tok[u] < 0) continue;
-      s *= ks[u] * p.sl2;
-      const float mn = fmaxf(m, s), mb = mn == -INFINITY ? 0.f : mn;
-      const float f = exp2f(m - mb), e = exp2f(s - mb);
-      l = l * f + e;
-      const float ev = e * vs[u];
-      const uint32_t vw[4] = {vu[u].x, vu[u].y, vu[u].z, vu[u].w};
+      for (int u = 0; u < BATCH; ++u) {
+        const uint32_t kw[4] = {ku[u].x, ku[u].y, ku[u].z, ku[u].w};
+        float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float vv[4];
-        from_e4m3x4(vw[i], vv);
+        for (int e = 0; e < 4; ++e) {
+          float kv[4];
+          from_e4m3x4(kw[e], kv);
 #pragma unroll
-        for (int z = 0; z < 4; ++z) acc[i * 4 + z] = fmaf(acc[i * 4 + z], f, ev * vv[z]);
+          for (int z = 0; z < 4; ++z) s = fmaf(q[e * 4 + z], kv[z], s);
+        }
+#pragma unroll
+        for (int o = LPT / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (tok[u] < 0) continue;
+        s *= ks[u] * p.sl2;
+        const float mn = fmaxf(m, s), mb = mn == -INFINITY ? 0.f : mn;
+        const float f = tc::ex2_approx(m - mb), e = tc::ex2_approx(s - mb);
+        l = l * f + e;
+        const float ev = e * vs[u];
+        const uint32_t vw[4] = {vu[u].x, vu[u].y, vu[u].z, vu[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float vv[4];
+          from_e4m3x4(vw[i], vv);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) acc[i * 4 + z] = fmaf(acc[i * 4 + z], f, ev * vv[z]);
+        }
+        m = mn;
       }
-      m = mn;
     }
   }
   if (part == 0) { gm[grp] = m; gl[grp] = l; }
 #pragma unroll
-  for (int e = 0; e < 16; ++e) go[grp][part * 16 + e] = acc[e];
+  for (int e = 0; e < 16; e += 4)
+    *reinterpret_cast<float4*>(&go[grp][part * 16 + e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
   __syncthreads();
   if (bad && tid == 0) report(p.status, SFA_ERR_INDEX);
   if (tid < D) {
     float M = -INFINITY, L = 0.f, o = 0.f;
+#pragma unroll 8
     for (int i = 0; i < GROUPS; ++i) M = fmaxf(M, gm[i]);
     const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll 8
     for (int i = 0; i < GROUPS; ++i) {
       const float f = exp2f(gm[i] - base);
       L += gl[i] * f;
@@ -319,10 +333,18 @@ cudaError_t launch_cache8_attn(const Cache8Attn& p, const CUtensorMap& tk, const
   return p.D == 128 ? launch_join_d<128>(p, st) : launch_join_d<64>(p, st);
 }
 
-cudaError_t launch_cache8_attn_list(const Cache8Attn& p, cudaStream_t st) {
+template <int D>
+static void launch_list(const Cache8Attn& p, cudaStream_t st) {
   const unsigned rows = (unsigned)(p.B * p.Hq);
-  if (p.D == 128) attn_list_kernel<128, 8><<<rows, 256, 0, st>>>(p);
-  else attn_list_kernel<64, 8><<<rows, 256, 0, st>>>(p);
+  // Up to two rows an SM: four tokens in flight a lane group (128 x 256 tokens: 5.5 us, 6.1 with two); more rows:
+  // two tokens and twice the CTAs a SM (512 x 1023 tokens: 33.5 us, 37.8 with four).
+  if (rows <= 2u * kSms) attn_list_kernel<D, 8, 4, 2><<<rows, 256, 0, st>>>(p);
+  else attn_list_kernel<D, 8, 2, 4><<<rows, 256, 0, st>>>(p);
+}
+
+cudaError_t launch_cache8_attn_list(const Cache8Attn& p, cudaStream_t st) {
+  if (p.D == 128) launch_list<128>(p, st);
+  else launch_list<64>(p, st);
   return cudaGetLastError();
 }
 

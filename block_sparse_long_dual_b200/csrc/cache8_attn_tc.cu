@@ -657,9 +657,8 @@ cudaError_t launch_t(const Cache8Attn& p, const CUtensorMap& tk, const CUtensorM
   static_assert(kCtasPerSm * L::TMEM <= 512, "tensor memory of an SM");
   static_assert(L::SUB * NC <= 32, "a lane of warp 0 for each factor");
   auto kern = attn_tile_kernel<D, NC, T>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::BYTES);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem_once(kern, L::BYTES, true, done);
   if (e != cudaSuccess) return e;
   kern<<<p.G, kTileThreads, L::BYTES, st>>>(tk, tv, p);
   return cudaGetLastError();

@@ -13,13 +13,14 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
 
+template <int THREADS>
 __device__ __forceinline__ uint32_t block_max(uint32_t x, uint32_t* sh) {
   x = __reduce_max_sync(0xffffffffu, x);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
   __syncthreads();
   uint32_t m = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) m = max(m, sh[w]);
+  for (int w = 0; w < THREADS / 32; ++w) m = max(m, sh[w]);
   return m;
 }
 
@@ -27,13 +28,18 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x, uint32_t* sh) {
 // append: a CTA per (touched block of T tokens, (b, KV head), K or V).  The new
 // rows of the block are read once into registers (16 bytes = 8 elements a
 // load), their largest magnitude gives the scale, and the codes leave from the
-// same registers.
+// same registers.  Bound by the bytes of the rows.  Load, reduce and store of one
+// CTA do not overlap, so the CTAs of an SM have to: 64 registers a thread, four CTAs
+// (a 131072-token prompt of 8 heads, 810 MB: 148 us, 84% of the measured copy rate;
+// 183 us with the compiler's choice of two, 153 with five).
 // ---------------------------------------------------------------------------
+constexpr int kAppend = 256;
+
 template <int D, int T>
-__global__ void __launch_bounds__(kThreads) append_kernel(Cache8Append p, int touched) {
+__global__ void __launch_bounds__(kAppend, 4) append_kernel(Cache8Append p, int touched) {
   constexpr int CPR = D / 8;                  // chunks of 8 elements per row
-  constexpr int CH = T * CPR / kThreads;      // chunks per thread
-  __shared__ uint32_t sh[kThreads / 32];
+  constexpr int CH = T * CPR / kAppend;      // chunks per thread
+  __shared__ uint32_t sh[kAppend / 32];
   const int unit = blockIdx.x / touched, bi = blockIdx.x % touched;
   const int b = unit / p.Hkv, kv = blockIdx.y, tid = threadIdx.x;
   const int at = p.at[b], cnt = p.counts ? p.counts[b] : p.n;
@@ -54,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Cache8Append p, int to
   uint32_t top = 0;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int i = tid + c * kThreads, row = row0 + i / CPR;
+    const int i = tid + c * kAppend, row = row0 + i / CPR;
     x[c] = make_uint4(0, 0, 0, 0);
     if (row >= at && row < end)
       x[c] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)(row - at) * D + (i % CPR) * 8));
@@ -69,14 +75,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Cache8Append p, int to
       if (hi < 0x7F800000u) top = max(top, hi);
     }
   }
-  top = block_max(top, sh);
+  top = block_max<kAppend>(top, sh);
   int ex = need_exp(top);
   const bool grown = row0 < at && ex > was;
   if (row0 < at && was > ex) ex = was;
   const float inv = pow2i(-ex);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int i = tid + c * kThreads, row = row0 + i / CPR;
+    const int i = tid + c * kAppend, row = row0 + i / CPR;
     if (row >= at && row < end) {
       const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
       uint32_t o[4];
@@ -163,7 +169,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
   __shared__ uint32_t sh_digit, sh_above;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = CS == 1 ? 0 : (int)cluster.block_rank();
-  const int unit = blockIdx.x / CS, b = unit / p.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int unit = blockIdx.x / CS, b = unit / p.Hkv, tid = threadIdx.x, lane = tid & 31;
   int n = p.lens[b];
   if (n < 0 || n > p.L) {
     if (tid == 0) report(p.status, SFA_ERR_INDEX);
@@ -323,8 +329,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
 
 template <int CS>
 static cudaError_t launch_select(const Cache8Evict& p, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<CS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)kSelSmem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem_once(evict_select_kernel<CS>, kSelSmem, false, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.dynamicSmemBytes = kSelSmem;
@@ -382,7 +388,7 @@ __global__ void __launch_bounds__(kThreads) evict_move_kernel(Cache8Evict p, int
     m = __vmaxu4(m, m >> 8) & 0x7Fu;
     if (m != 0) need = max(need, need_exp(__float_as_uint(__half2float(__low2half(from_e4m3x2(m))))) + ex[c]);
   }
-  need = (int)block_max((uint32_t)(need - kMinExp), sh) + kMinExp;
+  need = (int)block_max<kThreads>((uint32_t)(need - kMinExp), sh) + kMinExp;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     if (at[c] < 0) continue;
@@ -463,11 +469,11 @@ cudaError_t launch_cache8_append(const Cache8Append& p, cudaStream_t st) {
   if (gx > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)gx, 2);
   if (p.D == 128) {
-    if (p.T == 128) append_kernel<128, 128><<<grid, kThreads, 0, st>>>(p, nb);
-    else append_kernel<128, 64><<<grid, kThreads, 0, st>>>(p, nb);
+    if (p.T == 128) append_kernel<128, 128><<<grid, kAppend, 0, st>>>(p, nb);
+    else append_kernel<128, 64><<<grid, kAppend, 0, st>>>(p, nb);
   } else {
-    if (p.T == 128) append_kernel<64, 128><<<grid, kThreads, 0, st>>>(p, nb);
-    else append_kernel<64, 64><<<grid, kThreads, 0, st>>>(p, nb);
+    if (p.T == 128) append_kernel<64, 128><<<grid, kAppend, 0, st>>>(p, nb);
+    else append_kernel<64, 64><<<grid, kAppend, 0, st>>>(p, nb);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.in_place) return e;
