@@ -696,20 +696,12 @@ class FasaDecode:
 def _fits(t, name, shape, dtype, device):
     """Address of a buffer that _expect accepts (None: NULL).  The common case is tested here in one go (a decode
     step's calls are a few microseconds of GPU work each); anything else goes through _expect, which names what
-    is wrong.  ``device`` is the current device (_here)."""
+    is wrong.  ``device`` is the current device."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         _expect(t, name, shape, dtype, device)
     return t.data_ptr()
-
-
-def _here(cache):
-    """The cache's device, which must be the current one."""
-    dev = cache.k.device
-    if dev.index != torch.cuda.current_device():
-        _cuda(cache.k, "the cache")
-    return dev
 
 
 class KvCache8:
@@ -740,7 +732,9 @@ class KvCache8:
         self._c = Cache8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), lens.data_ptr(),
                          None if weight is None else weight.data_ptr(), block)
         self._cref = ctypes.byref(self._c)
-        self._shapes = {}
+        self._device, self._index = k.device, k.device.index
+        self._shapes = {}  # heads_q -> (Shape, reference to it)
+        self._kv_ref = self._shape_ref(Hkv)
         self._workspaces = {}
 
     @classmethod
@@ -756,16 +750,30 @@ class KvCache8:
                    weight=torch.zeros((batch, heads_kv, capacity), **kw) if weight else None, block=block)
 
     def shape(self, heads_q: int) -> Shape:
+        self._shape_ref(heads_q)
+        return self._shapes[heads_q][0]
+
+    def _shape_ref(self, heads_q):
         s = self._shapes.get(heads_q)
         if s is None:
-            s = self._shapes[heads_q] = Shape(self.batch, heads_q, self.heads_kv, self.capacity, self.head_dim, BF16)
-        return s
+            sh = Shape(self.batch, heads_q, self.heads_kv, self.capacity, self.head_dim, BF16)
+            s = self._shapes[heads_q] = (sh, ctypes.byref(sh))
+        return s[1]
+
+    def _launch(self, stream):
+        """(device, stream handle) for a call: the cache's device must be the current one."""
+        if torch.cuda.current_device() != self._index:
+            _cuda(self.k, "the cache")
+        if stream is None and _raw_stream is not None:
+            return self._device, _raw_stream(self._index)
+        return self._device, _stream(stream)
 
     def _status_ptr(self, status):
-        if status is self.status:
-            return status.data_ptr()
-        _status(status)
-        return None if status is None else status.data_ptr()
+        if status is None:
+            return None
+        if status is not self.status:
+            _status(status)
+        return status.data_ptr()
 
     def _workspace(self, q, weights):
         """The handle's own attention workspace for queries like q (one per shape, made on first use)."""
@@ -805,26 +813,27 @@ def cache8_append(cache: KvCache8, K, V, *, at=None, counts=None, status=None, s
     if K.dim() != 4:
         raise ValueError("K must be [B, Hkv, n, d]")
     n = K.shape[2]
-    dev = _here(cache)
+    dev, st = cache._launch(stream)
     rows, seqs = (cache.batch, cache.heads_kv, n, cache.head_dim), (cache.batch,)
-    _check(lib.sfa_cache8_append(ctypes.byref(cache.shape(cache.heads_kv)), cache._cref,
+    _check(lib.sfa_cache8_append(cache._kv_ref, cache._cref,
                                  _fits(K, "K", rows, torch.bfloat16, dev), _fits(V, "V", rows, torch.bfloat16, dev), n,
                                  _fits(at, "at", seqs, torch.int32, dev),
-                                 _fits(counts, "counts", seqs, torch.int32, dev), cache._status_ptr(status),
-                                 _stream(stream)), "sfa_cache8_append")
+                                 _fits(counts, "counts", seqs, torch.int32, dev), cache._status_ptr(status), st),
+           "sfa_cache8_append")
 
 
 def _cache8_query(q, cache: KvCache8):
-    """(shape, nq) of queries [B, Hq, d] or [B, Hq, nq, d]; checks q against the cache."""
-    if q.dim() not in (3, 4) or q.shape[0] != cache.batch or q.shape[-1] != cache.head_dim:
+    """(reference to the shape, nq) of queries [B, Hq, d] or [B, Hq, nq, d]; checks q against the cache."""
+    sizes = q.shape
+    if len(sizes) not in (3, 4) or sizes[0] != cache.batch or sizes[-1] != cache.head_dim:
         raise ValueError("q must be [B, Hq, d] or [B, Hq, nq, d] with the cache's B and d")
-    return cache.shape(q.shape[1]), (q.shape[2] if q.dim() == 4 else 1)
+    return cache._shape_ref(sizes[1]), (sizes[2] if len(sizes) == 4 else 1)
 
 
 def cache8_attn_workspace(q, cache: KvCache8, *, weights: bool = False) -> int:
     """Bytes of workspace cache8_attn needs for queries like q."""
     shape, nq = _cache8_query(q, cache)
-    n = int(load().sfa_cache8_attn_workspace(ctypes.byref(shape), nq, 1 if weights else 0))
+    n = int(load().sfa_cache8_attn_workspace(shape, nq, 1 if weights else 0))
     if n == 0:
         raise SfaError(4, "sfa_cache8_attn_workspace")
     return n
@@ -836,20 +845,21 @@ def cache8_attn(q, cache: KvCache8, *, back: int = 0, scale: float = 0.0, o=None
     cache; returns o.  With ``weight_out`` every token's attention weight is added to ``weight_in``."""
     lib = load()
     shape, nq = _cache8_query(q, cache)
-    dev = _here(cache)
+    dev, st = cache._launch(stream)
+    sizes = q.shape
     o = torch.empty_like(q) if o is None else o
     tokens = (cache.batch, cache.heads_kv, cache.capacity)
     if workspace is None:
         workspace = torch.empty(cache8_attn_workspace(q, cache, weights=weight_out is not None), dtype=torch.uint8,
                                 device=dev)
     nbytes = workspace.numel()
-    _check(lib.sfa_cache8_attn(ctypes.byref(shape), cache._cref, _fits(q, "q", q.shape, torch.bfloat16, dev), nq,
-                               back, scale, _fits(o, "o", q.shape, torch.bfloat16, dev),
-                               _fits(lse, "lse", q.shape[:-1], torch.float32, dev),
+    _check(lib.sfa_cache8_attn(shape, cache._cref, _fits(q, "q", sizes, torch.bfloat16, dev), nq, back, scale,
+                               _fits(o, "o", sizes, torch.bfloat16, dev),
+                               _fits(lse, "lse", sizes[:-1], torch.float32, dev),
                                _fits(weight_in, "weight_in", tokens, torch.float32, dev),
                                _fits(weight_out, "weight_out", tokens, torch.float32, dev),
                                _fits(workspace, "workspace", (nbytes,), torch.uint8, dev), nbytes,
-                               cache._status_ptr(status), _stream(stream)), "sfa_cache8_attn")
+                               cache._status_ptr(status), st), "sfa_cache8_attn")
     return o
 
 
@@ -859,20 +869,20 @@ def cache8_attn_list(q, cache: KvCache8, idx, *, scale: float = 0.0, o=None, lse
     if q.dim() != 3 or idx.dim() != 3:
         raise ValueError("q must be [B, Hq, d] and idx [B, Hq, k]")
     shape, _ = _cache8_query(q, cache)
-    dev = _here(cache)
+    dev, st = cache._launch(stream)
     o = torch.empty_like(q) if o is None else o
     rows, k = q.shape[:2], idx.shape[2]
-    _check(lib.sfa_cache8_attn_list(ctypes.byref(shape), cache._cref, _fits(q, "q", q.shape, torch.bfloat16, dev),
+    _check(lib.sfa_cache8_attn_list(shape, cache._cref, _fits(q, "q", q.shape, torch.bfloat16, dev),
                                     _fits(idx, "idx", (*rows, k), torch.int32, dev), k, scale,
                                     _fits(o, "o", q.shape, torch.bfloat16, dev),
-                                    _fits(lse, "lse", rows, torch.float32, dev), cache._status_ptr(status),
-                                    _stream(stream)), "sfa_cache8_attn_list")
+                                    _fits(lse, "lse", rows, torch.float32, dev), cache._status_ptr(status), st),
+           "sfa_cache8_attn_list")
     return o
 
 
 def cache8_evict_workspace(src: KvCache8, keep: int) -> int:
     """Bytes of workspace cache8_evict needs."""
-    n = int(load().sfa_cache8_evict_workspace(ctypes.byref(src.shape(src.heads_kv)), int(keep)))
+    n = int(load().sfa_cache8_evict_workspace(src._kv_ref, int(keep)))
     if n == 0:
         raise SfaError(1, "sfa_cache8_evict_workspace")
     return n
@@ -883,7 +893,7 @@ def cache8_evict(src: KvCache8, dst: KvCache8, *, keep: int, recent: int = 0, id
     """sfa_cache8_evict: the last ``recent`` tokens and those of the largest ``src.weight``, ``keep`` in all,
     move to ``dst``; returns idx [B, Hkv, keep] int32, their rows in src (ascending, -1 padded)."""
     lib = load()
-    dev = _here(src)
+    dev, st = src._launch(stream)
     if (dst.batch, dst.heads_kv, dst.head_dim) != (src.batch, src.heads_kv, src.head_dim):
         raise ValueError("dst must have the batch, heads and head dim of src")
     if dst.k.device != dev:
@@ -891,10 +901,10 @@ def cache8_evict(src: KvCache8, dst: KvCache8, *, keep: int, recent: int = 0, id
     if idx is None:
         idx = torch.empty((src.batch, src.heads_kv, max(int(keep), 0)), dtype=torch.int32, device=dev)
     nbytes = 0 if workspace is None else workspace.numel()
-    _check(lib.sfa_cache8_evict(ctypes.byref(src.shape(src.heads_kv)), src._cref, dst._cref, dst.capacity, keep, recent,
+    _check(lib.sfa_cache8_evict(src._kv_ref, src._cref, dst._cref, dst.capacity, keep, recent,
                                 _fits(idx, "idx", (src.batch, src.heads_kv, keep), torch.int32, dev),
                                 _fits(workspace, "workspace", (nbytes,), torch.uint8, dev), nbytes,
-                                src._status_ptr(status), _stream(stream)), "sfa_cache8_evict")
+                                src._status_ptr(status), st), "sfa_cache8_evict")
     return idx
 
 
@@ -906,13 +916,12 @@ def cache8_fc_gather(cache: KvCache8, fc, *, K_fc=None, pos0: int = 0, npos: int
     if pairs.ndim != 2 or pairs.shape[0] != cache.heads_kv:
         raise ValueError("fc must be [heads_kv, nfc]")
     nfc = pairs.shape[1]
-    dev = _here(cache)
+    dev, st = cache._launch(stream)
     rows = (cache.batch, cache.heads_kv, cache.capacity, 2 * nfc)
     K_fc = torch.empty(rows, dtype=torch.bfloat16, device=dev) if K_fc is None else K_fc
     npos = cache.capacity - pos0 if npos is None else npos
-    _check(lib.sfa_cache8_fc_gather(ctypes.byref(cache.shape(cache.heads_kv)), cache._cref, pairs.ctypes.data, nfc, pos0,
-                                    npos, _fits(K_fc, "K_fc", rows, torch.bfloat16, dev), _stream(stream)),
-           "sfa_cache8_fc_gather")
+    _check(lib.sfa_cache8_fc_gather(cache._kv_ref, cache._cref, pairs.ctypes.data, nfc, pos0, npos,
+                                    _fits(K_fc, "K_fc", rows, torch.bfloat16, dev), st), "sfa_cache8_fc_gather")
     return K_fc
 
 
