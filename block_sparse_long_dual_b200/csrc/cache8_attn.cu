@@ -14,9 +14,10 @@ using namespace c8;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------------------
-// Joining the pieces.  The first B Hkv cols CTAs each join one query row of one
-// unit (a thread per dim, the row's pieces shared among the thread groups); the
-// others, with weights, each add the attention weights of some chunks of tokens
+// Joining the pieces.  The first CTAs each join one query row of one unit (a
+// thread per dim, the row's pieces shared among the thread groups) or, where there
+// are rows enough to fill the SMs without that, all rows of a unit, a thread group
+// a row; the others, with weights, each add the attention weights of some chunks of tokens
 // of one unit: the rows' log-sum-exps again from the pieces' maxima and sums (a few
 // numbers), then exp2 of the scores that the first step left, summed over the
 // rows in order.  Launched while the first step still runs: everything up to
@@ -29,7 +30,7 @@ __device__ __forceinline__ void pieces_ready() { asm volatile("griddepcontrol.wa
 // Tokens per thread of the weights part: about eight 16-byte loads of scores in flight.
 constexpr int weight_tokens(int CP) { return CP <= 4 ? 8 : (CP == 8 ? 4 : 2); }
 
-template <int D, int CP>  // CP = p.cpad
+template <int D, int CP, bool UNIT>  // CP = p.cpad; UNIT: a joining CTA takes all rows of a unit
 __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid_constant__ Cache8Attn p, int parts,
                                                                    int per_part) {
   constexpr int GR = kJoinThreads / D;  // thread groups
@@ -38,9 +39,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
   __shared__ float so[GR][D], sl[GR];
   __shared__ __align__(16) float slse[kMaxCols];
   const int tid = threadIdx.x;
-  const unsigned rows = (unsigned)(p.B * p.Hkv * p.cols);
+  const unsigned rows = (unsigned)(p.B * p.Hkv * (UNIT ? 1 : p.cols));  // joining CTAs
   const bool join = blockIdx.x < rows;
-  const int unit = join ? blockIdx.x / p.cols : (blockIdx.x - rows) / parts;
+  const int unit = join ? blockIdx.x / (UNIT ? 1 : p.cols) : (blockIdx.x - rows) / parts;
   const int b = unit / p.Hkv, g = unit % p.Hkv;
   const int nv = visible(p.lens, b, p.L, p.back, nullptr);
   const int tiles = (nv + p.tile - 1) / p.tile;
@@ -63,6 +64,26 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
   }
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   pieces_ready();
+  if (join && UNIT) {
+    const int grp = tid / D, r = tid % D;
+    for (int c = grp; c < p.cols; c += GR) {
+      float M = -INFINITY, l = 0.f, o = 0.f;
+      for (int i = 0; i < np; ++i) {
+        const size_t at = (s0 + i) * p.cols + c;
+        const float2 x = ml[at];
+        const float v = p.part_o[at * D + r], mn = fmaxf(M, x.x), base = mn == -INFINITY ? 0.f : mn;
+        const float keep = exp2f(M - base), f = exp2f(x.x - base);
+        l = fmaf(x.y, f, l * keep);
+        o = fmaf(v, f, o * keep);
+        M = mn;
+      }
+      // l = 0 exactly when the row sees no token (a NaN score makes l NaN, and the row's o)
+      const size_t row = (size_t)unit * p.cols + c;
+      static_cast<__nv_bfloat16*>(p.o)[row * D + r] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+      if (r == 0 && p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(l)) * kLn2;
+    }
+    return;
+  }
   if (join) {
     const int c = blockIdx.x % p.cols, grp = tid / D, r = tid % D;
     float M = -INFINITY;
@@ -164,7 +185,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
   }
 }
 
-template <int D, int CP>
+template <int D, int CP, bool UNIT>
 static cudaError_t launch_join(const Cache8Attn& p, cudaStream_t st) {
   // The weights part: CTAs of whole chunks, about four CTAs per SM in all (each pays its start once).
   const int chunk = weight_tokens(CP) * kJoinThreads, chunks = (p.L + chunk - 1) / chunk;
@@ -173,7 +194,7 @@ static cudaError_t launch_join(const Cache8Attn& p, cudaStream_t st) {
   each = each < 1 ? 1 : (each > chunks ? chunks : each);
   const int parts = (int)((chunks + each - 1) / each);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.B * p.Hkv * (p.cols + (p.w_out != nullptr ? parts : 0)));
+  cfg.gridDim = dim3((unsigned)p.B * p.Hkv * ((UNIT ? 1 : p.cols) + (p.w_out != nullptr ? parts : 0)));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -181,18 +202,25 @@ static cudaError_t launch_join(const Cache8Attn& p, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, CP>, p, parts, (int)each * chunk);
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, CP, UNIT>, p, parts, (int)each * chunk);
+}
+
+template <int D, int CP>
+static cudaError_t launch_join_u(const Cache8Attn& p, cudaStream_t st) {
+  // A CTA a row while they are resident at once, four to an SM; more rows: a CTA a unit (24 sequences x 8 heads of 8
+  // rows with weights: the whole call 48.8 against 54.5 us; 16 x 8 of 4 rows: 166 against 164.6).
+  return (long long)p.B * p.Hkv * p.cols > 4 * kSms ? launch_join<D, CP, true>(p, st) : launch_join<D, CP, false>(p, st);
 }
 
 template <int D>
 static cudaError_t launch_join_d(const Cache8Attn& p, cudaStream_t st) {
   switch (p.cpad) {
-    case 1: return launch_join<D, 1>(p, st);
-    case 2: return launch_join<D, 2>(p, st);
-    case 4: return launch_join<D, 4>(p, st);
-    case 8: return launch_join<D, 8>(p, st);
-    case 12: return launch_join<D, 12>(p, st);
-    default: return launch_join<D, 16>(p, st);
+    case 1: return launch_join_u<D, 1>(p, st);
+    case 2: return launch_join_u<D, 2>(p, st);
+    case 4: return launch_join_u<D, 4>(p, st);
+    case 8: return launch_join_u<D, 8>(p, st);
+    case 12: return launch_join_u<D, 12>(p, st);
+    default: return launch_join_u<D, 16>(p, st);
   }
 }
 

@@ -21,7 +21,8 @@
 //                 memory), probabilities as e4m3 into shared memory; thread r = dim r
 //                 for O^T: the running O of the piece in registers.  O^T of tile j - 1
 //                 is added after the probabilities of tile j are on their way.
-//   warp 4        producer: TMA tiles of K and V (a ring each)
+//   warp 4        O's factors of each tile, out of the way of the softmax warps, and the
+//                 producer: TMA tiles of K and V (a ring each)
 //   warp 5        MMA issuer
 // A tile is 32 KB (128 tokens of d = 128, 256 of d = 64: with 128 tokens the softmax
 // warps, a chain of latencies, set the pace of the smaller rows) and 8 to 12 MMAs of
@@ -31,6 +32,7 @@
 // waits return at once and the CTA runs to its end (the copies and MMAs it issued
 // are drained).
 #include <cuda.h>
+#include <float.h>
 #include <math.h>
 
 #include "cache8.cuh"
@@ -64,19 +66,18 @@ struct Lay {
   static constexpr uint32_t OFF_EV = OFF_P + 2 * PB;                 // edge tokens' V rows, two buffers
   static constexpr uint32_t OFF_EE = OFF_EV + 2 * kEdge * D;         // their probabilities [2][kEdge][NC]
   static constexpr uint32_t OFF_MAX = OFF_EE + 2 * kEdge * NC * 4;   // warp maxima [2][H][4][NC]
-  static constexpr uint32_t OFF_FAC = OFF_MAX + 2 * H * 4 * NC * 4;  // [2][NC] keep, [2][SUB][NC] f, [2][SUB][NC] f v
-  static constexpr uint32_t OFF_QF = OFF_FAC + 2 * NC * (1 + 2 * SUB) * 4;  // row factors [2][NC]
+  static constexpr uint32_t OFF_FAC = OFF_MAX + 2 * H * 4 * NC * 4;  // [2][NC] keep, [2][SUB][NC] f,
+                                                                     // [2][SUB][NC] f v, [NC] running maxima
+  static constexpr uint32_t OFF_QF = OFF_FAC + NC * (3 + 4 * SUB) * 4;  // row factors [2][NC]
   static constexpr uint32_t OFF_BAR = OFF_QF + 2 * NC * 4;
-  static constexpr int B0 = 2 * NK + 2 * NV, NBAR = B0 + 9;
+  static constexpr int B0 = NK + NV, NBAR = B0 + 9;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t BYTES = OFF_MISC + 64 + 1024;
   // TMEM columns: S two buffers of H parts, O two buffers of SUB parts
   static constexpr uint32_t COL_O = 2 * H * N, COLS_USED = COL_O + 2 * SUB * N;
   static constexpr uint32_t TMEM = COLS_USED <= 64 ? 64 : (COLS_USED <= 128 ? 128 : 256);
   __host__ __device__ static constexpr int kf(int s) { return s; }
-  __host__ __device__ static constexpr int ke(int s) { return NK + s; }
-  __host__ __device__ static constexpr int vf(int s) { return 2 * NK + s; }
-  __host__ __device__ static constexpr int ve(int s) { return 2 * NK + NV + s; }
+  __host__ __device__ static constexpr int vf(int s) { return NK + s; }
   __host__ __device__ static constexpr int sf(int b) { return B0 + b; }
   __host__ __device__ static constexpr int pf(int b) { return B0 + 2 + b; }
   __host__ __device__ static constexpr int of(int b) { return B0 + 4 + b; }
@@ -159,6 +160,21 @@ __device__ __forceinline__ void load_row(const float* p, float (&v)[NC]) {
   }
 }
 
+// The same as packed pairs (float32 pair arithmetic: half the instructions of the tile loop's sums and products).
+template <int NC>
+__device__ __forceinline__ void load_pairs(const float* p, uint64_t (&v)[NC / 2]) {
+#pragma unroll
+  for (int c = 0; c < NC; c += 4) {
+    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(p + c);
+    v[c / 2] = u.x;
+    v[c / 2 + 1] = u.y;
+  }
+}
+__device__ __forceinline__ uint64_t pair(float x) { return tc::f2_pack(x, x); }
+__device__ __forceinline__ uint64_t pair_bits(uint32_t a, uint32_t b) {
+  return tc::f2_pack(__uint_as_float(a), __uint_as_float(b));
+}
+
 template <int N>
 __device__ __forceinline__ void tmem_row(uint32_t at, uint32_t (&v)[N]) {
   static_assert(N == 16 || N == 32, "two columns a query row");
@@ -166,7 +182,23 @@ __device__ __forceinline__ void tmem_row(uint32_t at, uint32_t (&v)[N]) {
   else tc::tmem_ld32(at, v);
 }
 
+// The softmax warps; and with the factor warp: once a tile, and once at a piece's end.
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void tile_sync() { asm volatile("bar.sync 2, 160;" ::: "memory"); }
+
+// The share's tiles one by one: first row of each in the code arrays.
+template <int TILE_T>
+struct TileRows {
+  Pieces<TILE_T> pc;
+  int tile;
+  __device__ int take(const Cache8Attn& p) {
+    if (tile == pc.last) {
+      pc.next(p);
+      tile = pc.first;
+    }
+    return (pc.b * p.Hkv + pc.g) * p.L + TILE_T * tile++;
+  }
+};
 
 // Query rows of one unit as two e4m3 parts: B operand, K-major, no swizzle (8 rows x 16 bytes contiguous).
 template <int D, int NC, int T>
@@ -266,33 +298,82 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
     Pieces<TILE_T> pc;
     pc.begin(sched[0], sched[1], sched[3], n);
     if (warp == 4) {
-      // ------------------------------ producer ------------------------------
+      // ------------------------ factors and copies --------------------------
+      const float* smax = reinterpret_cast<const float*>(sm + L::OFF_MAX);
+      float* fkeep = reinterpret_cast<float*>(sm + L::OFF_FAC);
+      float* ff = fkeep + 2 * NC;
+      float* ffv = ff + 2 * SUB * NC;
+      float* fmax_row = ffv + 2 * SUB * NC;
+      constexpr int WPS = T / 32;  // warps per scale block
+      const int fc = lane % NC, fs = lane / NC;  // this lane: row fc, scale block fs of the tile
+      const bool mine = fs < SUB;
+      TileRows<TILE_T> kr{pc, pc.first}, vr{pc, pc.first};
+      const uint64_t once = tc::policy_evict_first();  // leaves L2 to the scores, queries and pieces (2%)
+      const uint32_t tiles = (uint32_t)n;
+      uint32_t nk = 0, nv = 0;  // K and V tiles whose copy has been started (lane 0)
+      auto load_k = [&] {
+        const uint32_t s = nk % NK;
+        tc::mbar_arrive_expect_tx(cx.bar(L::kf(s)), L::TILE);
+        tc::tma_load_2d_hint(sb + L::OFF_K + s * L::TILE, &tmK, cx.bar(L::kf(s)), 0, kr.take(p), once);
+        ++nk;
+      };
+      auto load_v = [&] {
+        const uint32_t s = nv % NV;
+        tc::mbar_arrive_expect_tx(cx.bar(L::vf(s)), L::TILE);
+        tc::tma_load_2d_hint(sb + L::OFF_V + s * L::TILE, &tmV, cx.bar(L::vf(s)), 0, vr.take(p), once);
+        ++nv;
+      };
       if (lane == 0) {
-        uint32_t j = 0;
-        bool ok = true;
-        const uint64_t once = tc::policy_evict_first();  // leaves L2 to the scores, queries and pieces (2%)
-        do {
-          const int row0 = (pc.b * p.Hkv + pc.g) * p.L;
-          for (int t = pc.first; ok && t < pc.last; ++t, ++j) {
-            const uint32_t sk = j % NK, sv = j % NV;
-            if (j >= NK && !wait(cx, cx.bar(L::ke(sk)), ((j / NK) & 1) ^ 1)) { ok = false; break; }
-            tc::mbar_arrive_expect_tx(cx.bar(L::kf(sk)), L::TILE);
-            tc::tma_load_2d_hint(sb + L::OFF_K + sk * L::TILE, &tmK, cx.bar(L::kf(sk)), 0, row0 + t * TILE_T,
-                                 once);
-            if (j >= NV && !wait(cx, cx.bar(L::ve(sv)), ((j / NV) & 1) ^ 1)) {
-              drain(cx.bar(L::kf(sk)), (j / NK) & 1);
-              ok = false;
-              break;
-            }
-            tc::mbar_arrive_expect_tx(cx.bar(L::vf(sv)), L::TILE);
-            tc::tma_load_2d_hint(sb + L::OFF_V + sv * L::TILE, &tmV, cx.bar(L::vf(sv)), 0, row0 + t * TILE_T,
-                                 once);
-          }
-        } while (ok && pc.next(p));
-        if (*cx.abort_flag) {  // every copy that was started lands before the CTA exits
-          for (uint32_t i = j > NK ? j - NK : 0; i < j; ++i) drain(cx.bar(L::kf(i % NK)), (i / NK) & 1);
-          for (uint32_t i = j > NV ? j - NV : 0; i < j; ++i) drain(cx.bar(L::vf(i % NV)), (i / NV) & 1);
+        for (uint32_t i = 0; i < NK && i < tiles; ++i) {
+          load_k();
+          if (i < NV) load_v();
         }
+      }
+      uint32_t j = 0;
+      for (;;) {
+        const int blk0 = (pc.b * p.Hkv + pc.g) * p.nblk;
+        float vs_next = 0.f, M = -INFINITY;  // M: running maximum of row fc
+        auto load_scale = [&](int tile) {
+          const int t = tile * TILE_T + fs * T;
+          vs_next = mine && t < pc.nv ? __ldg(p.vs + blk0 + t / T) * (1.f / kTopP) : 0.f;
+        };
+        load_scale(pc.first);
+        for (int tile = pc.first; tile < pc.last; ++tile, ++j) {
+          const float vs = vs_next;
+          if (tile + 1 < pc.last) load_scale(tile + 1);
+          tile_sync();
+          const float* wm = smax + (j & 1) * H * 4 * NC;
+          float mt = -INFINITY;
+          if (mine) {
+#pragma unroll
+            for (int w = 0; w < WPS; ++w) mt = fmaxf(mt, wm[(fs * WPS + w) * NC + fc]);
+          }
+          float mn = fmaxf(M, mt);
+#pragma unroll
+          for (int o = NC; o < NC * SUB; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+          if (mine) {
+            const float f = mt == -INFINITY ? 0.f : tc::ex2_approx(mt - mn);
+            if (fs == 0) {
+              fkeep[(j & 1) * NC + fc] = M == -INFINITY ? 0.f : tc::ex2_approx(M - mn);
+              fmax_row[fc] = mn;
+            }
+            ff[((j & 1) * SUB + fs) * NC + fc] = f;
+            ffv[((j & 1) * SUB + fs) * NC + fc] = f * vs;
+          }
+          M = mn;
+          if (lane == 0) {
+            // Every softmax thread has S(j): its MMAs are done with K(j)'s stage.  O(j - 1) complete: so is V(j - 1)'s.
+            if (nk < tiles) load_k();
+            if (j > 0 && nv < tiles && wait(cx, cx.bar(L::of((j - 1) & 1)), ((j - 1) >> 1) & 1)) load_v();
+          }
+          __syncwarp();
+        }
+        tile_sync();
+        if (!pc.next(p)) break;
+      }
+      if (lane == 0 && *cx.abort_flag) {  // every copy that was started lands before the CTA exits
+        for (uint32_t i = nk > NK ? nk - NK : 0; i < nk; ++i) drain(cx.bar(L::kf(i % NK)), (i / NK) & 1);
+        for (uint32_t i = nv > NV ? nv - NV : 0; i < nv; ++i) drain(cx.bar(L::vf(i % NV)), (i / NV) & 1);
       }
     } else if (warp == 5) {
       // ------------------------------ MMA issuer ----------------------------
@@ -325,7 +406,6 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
             for (int i = 0; i < D / 32; ++i)
               tc::mma_e4m3_ss(tmem + ((j & 1) * H + h) * N, tc::smem_desc(k + h * 128 * D + i * 32, 16, ROWS8, SWZ),
                               tc::smem_desc(q + i * 256, 128, D * 8, 0), id_qk, i > 0);
-          tc::mma_commit(cx.bar(L::ke(s)));
           tc::mma_commit(cx.bar(L::sf(j & 1)));
           return true;
         };
@@ -345,7 +425,6 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
             tc::mma_e4m3_ss(tmem + L::COL_O + ((j & 1) * SUB + i / (T / 32)) * N,
                             tc::smem_desc(v + i * 4 * ROWS8, ROWS8, ROWS8, SWZ),
                             tc::smem_desc(pp + i * 512, 128, TILE_T * 16, 0), id_pv, i % (T / 32) > 0);
-          tc::mma_commit(cx.bar(L::ve(s)));
           tc::mma_commit(cx.bar(L::of(j & 1)));
           if (j + 2 < tiles) ok = issue_s(j + 2);
         }
@@ -355,17 +434,15 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
     } else {
       // ------------------------- softmax and O ------------------------------
       float* smax = reinterpret_cast<float*>(sm + L::OFF_MAX);    // [2][H][4][NC]
-      float* fkeep = reinterpret_cast<float*>(sm + L::OFF_FAC);   // [2][NC]
-      float* ff = fkeep + 2 * NC;                                 // [2][SUB][NC]
-      float* ffv = ff + 2 * SUB * NC;                             // [2][SUB][NC]
+      const float* fkeep = reinterpret_cast<const float*>(sm + L::OFF_FAC);  // [2][NC]
+      const float* ff = fkeep + 2 * NC;                           // [2][SUB][NC]
+      const float* ffv = ff + 2 * SUB * NC;                       // [2][SUB][NC]
+      const float* fmax_row = ffv + 2 * SUB * NC;                 // [NC]
       float* ee = reinterpret_cast<float*>(sm + L::OFF_EE);       // [2][kEdge][NC]
       const float* qfac = reinterpret_cast<const float*>(sm + L::OFF_QF);
       const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
       constexpr int WPS = T / 32;  // warps per scale block
       const int my_sub = tid / T;  // scale block of this thread's token within its 128
-      // Lane fs NC + fc of warp 0 keeps row fc's running maximum and works out its factor for block fs.
-      const int fc = lane % NC, fs = lane / NC;
-      const bool factors = warp == 0 && fs < SUB;
       uint32_t j = 0, piece = 0;
 
       write_q<D, NC, T>(p, sm, 0, pc.b * p.Hkv + pc.g, tid);
@@ -377,26 +454,24 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
         const int unit = pc.b * p.Hkv + pc.g;
         const int blk0 = unit * p.nblk;  // B Hkv blocks stay under 2^31
         // The scales of a tile are loaded a tile ahead.
-        float ks_next[H], vs_next = 0.f;
+        float ks_next[H];
         auto load_scales = [&](int tile) {
 #pragma unroll
           for (int h = 0; h < H; ++h) {
             const int t = tile * TILE_T + h * 128 + tid;
             ks_next[h] = t < pc.nv ? __ldg(p.ks + blk0 + t / T) : 0.f;
           }
-          const int tv = tile * TILE_T + fs * T;
-          if (factors) vs_next = tv < pc.nv ? __ldg(p.vs + blk0 + tv / T) * (1.f / kTopP) : 0.f;
         };
         load_scales(pc.first);
         softmax_sync();  // this piece's row factors, written by other warps
-        float l[NC], acc[NC], e_prev[H][NC];
+        constexpr int NP = NC / 2;
+        uint64_t l[NP], acc[NP], e_prev[H][NP];  // pairs of rows
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          l[c] = acc[c] = 0.f;
+        for (int c = 0; c < NP; ++c) {
+          l[c] = acc[c] = 0;
 #pragma unroll
-          for (int h = 0; h < H; ++h) e_prev[h][c] = 0.f;
+          for (int h = 0; h < H; ++h) e_prev[h][c] = 0;
         }
-        float M = -INFINITY;     // running maximum of row fc
         int edge_prev = TILE_T;  // first edge token of the previous tile
         int edge_n = 0;          // and how many
         // Adds O^T of tile i to the registers, and the tile's probabilities to l.
@@ -410,19 +485,19 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
 #pragma unroll
           for (int s = 0; s < BOTH; ++s) tmem_row<N>(at + s * N, o[s]);
           {
-            float kp[NC];
-            load_row<NC>(fkeep + (i & 1) * NC, kp);
+            uint64_t kp[NP];
+            load_pairs<NC>(fkeep + (i & 1) * NC, kp);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              acc[c] *= kp[c];
-              l[c] *= kp[c];
+            for (int c = 0; c < NP; ++c) {
+              acc[c] = tc::f2_mul(acc[c], kp[c]);
+              l[c] = tc::f2_mul(l[c], kp[c]);
             }
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-              float fp[NC];
-              load_row<NC>(ff + ((i & 1) * SUB + h * SUBH + my_sub) * NC, fp);
+              uint64_t fp[NP];
+              load_pairs<NC>(ff + ((i & 1) * SUB + h * SUBH + my_sub) * NC, fp);
 #pragma unroll
-              for (int c = 0; c < NC; ++c) l[c] = fmaf(e_prev[h][c], fp[c], l[c]);
+              for (int c = 0; c < NP; ++c) l[c] = tc::f2_fma(e_prev[h][c], fp[c], l[c]);
             }
           }
           const float* vp = ffv + (i & 1) * SUB * NC;
@@ -436,12 +511,14 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
             tc::tmem_wait_ld();
 #pragma unroll
             for (int s = 0; s < BOTH; ++s) {
-              float fv[NC];
-              load_row<NC>(vp + (s0 + s) * NC, fv);
+              uint64_t fv[NP];
+              load_pairs<NC>(vp + (s0 + s) * NC, fv);
 #pragma unroll
-              for (int c = 0; c < NC; ++c)
-                acc[c] = fmaf(fmaf(__uint_as_float(o[s][NC + c]), 1.f / kLoP, __uint_as_float(o[s][c])), fv[c],
-                              acc[c]);
+              for (int c = 0; c < NP; ++c) {
+                const uint64_t x = tc::f2_fma(pair_bits(o[s][NC + 2 * c], o[s][NC + 2 * c + 1]), pair(1.f / kLoP),
+                                              pair_bits(o[s][2 * c], o[s][2 * c + 1]));
+                acc[c] = tc::f2_fma(x, fv[c], acc[c]);
+              }
             }
           }
           for (int r = 0; r < edge_n; ++r) {
@@ -449,8 +526,13 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
             const float* er = ee + ((i & 1) * kEdge + r) * NC;
             const float* vr = vp + ((edge_prev + r) / T) * NC;
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if (!(er[c] < 0.f)) acc[c] = fmaf(er[c] * vr[c], v, acc[c]);  // < 0: the row does not see it
+            for (int c = 0; c < NP; ++c) {
+              float a0, a1;
+              tc::f2_unpack(acc[c], a0, a1);
+              if (!(er[2 * c] < 0.f)) a0 = fmaf(er[2 * c] * vr[2 * c], v, a0);  // < 0: the row does not see it
+              if (!(er[2 * c + 1] < 0.f)) a1 = fmaf(er[2 * c + 1] * vr[2 * c + 1], v, a1);
+              acc[c] = tc::f2_pack(a0, a1);
+            }
           }
           tc::tc_fence_before();
         };
@@ -461,23 +543,25 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
           float ks[H];
 #pragma unroll
           for (int h = 0; h < H; ++h) ks[h] = ks_next[h];
-          const float vs = vs_next;
           if (tile + 1 < pc.last) load_scales(tile + 1);
           wait(cx, cx.bar(L::sf(j & 1)), (j >> 1) & 1);
           __syncwarp();
           tc::tc_fence_after();
           float e[H][NC];  // scores in log2 units, then probabilities against the block's maximum
           {
-            float qf[NC];
-            load_row<NC>(qfac + (piece & 1) * NC, qf);
+            uint64_t qf[NP];
+            load_pairs<NC>(qfac + (piece & 1) * NC, qf);
 #pragma unroll
             for (int h = 0; h < H; ++h) {
               uint32_t r[N];
               tmem_row<N>(tmem + lane_base + ((j & 1) * H + h) * N, r);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < NC; ++c)
-                e[h][c] = fmaf(__uint_as_float(r[NC + c]), 1.f / kLoQ, __uint_as_float(r[c])) * (ks[h] * qf[c]);
+              for (int c = 0; c < NP; ++c) {
+                const uint64_t x = tc::f2_fma(pair_bits(r[NC + 2 * c], r[NC + 2 * c + 1]), pair(1.f / kLoQ),
+                                              pair_bits(r[2 * c], r[2 * c + 1]));
+                tc::f2_unpack(tc::f2_mul(x, tc::f2_mul(pair(ks[h]), qf[c])), e[h][2 * c], e[h][2 * c + 1]);
+              }
             }
           }
           if (edge < TILE_T) {  // only here some row does not see some token; rows from cols on are never used
@@ -494,13 +578,14 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
           float* wm = smax + (j & 1) * H * 4 * NC;
 #pragma unroll
           for (int h = 0; h < H; ++h) {
-            float mine = 0.f;
+            float m[NC];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              const float m = tc::warp_max(e[h][c]);
-              if (lane == c) mine = m;
+            for (int c = 0; c < NC; ++c) m[c] = tc::warp_max(e[h][c]);
+            if (lane == 0) {
+#pragma unroll
+              for (int c = 0; c < NC; c += 4)
+                *reinterpret_cast<float4*>(wm + (h * 4 + warp) * NC + c) = make_float4(m[c], m[c + 1], m[c + 2], m[c + 3]);
             }
-            if (lane < NC) wm[(h * 4 + warp) * NC + lane] = mine;
           }
           if (p.scores != nullptr) {
 #pragma unroll
@@ -520,34 +605,34 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
               }
             }
           }
-          softmax_sync();
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            float m[NC];
-            load_row<NC>(wm + (h * 4 + my_sub * WPS) * NC, m);
-#pragma unroll
-            for (int w = 1; w < WPS; ++w) {
-              float u[NC];
-              load_row<NC>(wm + (h * 4 + my_sub * WPS + w) * NC, u);
-#pragma unroll
-              for (int c = 0; c < NC; ++c) m[c] = fmaxf(m[c], u[c]);
-            }
-#pragma unroll
-            for (int c = 0; c < NC; ++c) e[h][c] = tc::ex2_approx(e[h][c] - (m[c] == -INFINITY ? 0.f : m[c]));
-          }
+          tile_sync();
           // Probabilities as two e4m3 parts: B operand, MN-major, no swizzle (8 tokens x 16 rows contiguous).
 #pragma unroll
           for (int h = 0; h < H; ++h) {
+            float m[WPS][NC];
+#pragma unroll
+            for (int w = 0; w < WPS; ++w) load_row<NC>(wm + (h * 4 + my_sub * WPS + w) * NC, m[w]);
             uint32_t hi[NC / 4], lo[NC / 4];
 #pragma unroll
             for (int c = 0; c < NC; c += 4) {
               uint32_t h2[2], l2[2];
 #pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                // A block without a score: against the lowest float, exp2(-inf) = 0.
+                float mx = tc::max3(m[0][c + u], m[1][c + u], -FLT_MAX);
+                if (WPS == 4) mx = tc::max3(mx, m[WPS - 2][c + u], m[WPS - 1][c + u]);
+                e[h][c + u] = tc::ex2_approx(e[h][c + u] - mx);
+              }
+#pragma unroll
               for (int u = 0; u < 2; ++u) {
-                const float a = e[h][c + 2 * u] * kTopP, b = e[h][c + 2 * u + 1] * kTopP;
+                const uint64_t x = tc::f2_pack(e[h][c + 2 * u], e[h][c + 2 * u + 1]);
+                float a, b;
+                tc::f2_unpack(tc::f2_mul(x, pair(kTopP)), a, b);
                 h2[u] = to_e4m3x2(a, b);
                 const float2 f = __half22float2(from_e4m3x2(h2[u]));
-                l2[u] = to_e4m3x2((a - f.x) * kLoP, (b - f.y) * kLoP);
+                // (a - f) kLoP, exact up to the last rounding
+                tc::f2_unpack(tc::f2_fma(tc::f2_pack(f.x, f.y), pair(-kLoP), tc::f2_mul(x, pair(kTopP * kLoP))), a, b);
+                l2[u] = to_e4m3x2(a, b);
               }
               hi[c / 4] = h2[0] | (h2[1] << 16);
               lo[c / 4] = l2[0] | (l2[1] << 16);
@@ -585,23 +670,6 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
           tc::fence_proxy_async_smem();
           tc::tc_fence_before();
           tc::mbar_arrive(cx.bar(L::pf(j & 1)));
-          if (warp == 0) {  // factors of row fc: the new running maximum, block fs against it
-            float mt = -INFINITY;
-            if (factors) {
-#pragma unroll
-              for (int w = 0; w < WPS; ++w) mt = fmaxf(mt, wm[(fs * WPS + w) * NC + fc]);
-            }
-            float mn = fmaxf(M, mt);
-#pragma unroll
-            for (int o = NC; o < NC * SUB; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-            if (factors) {
-              const float f = mt == -INFINITY ? 0.f : tc::ex2_approx(mt - mn);
-              if (fs == 0) fkeep[(j & 1) * NC + fc] = M == -INFINITY ? 0.f : tc::ex2_approx(M - mn);
-              ff[((j & 1) * SUB + fs) * NC + fc] = f;
-              ffv[((j & 1) * SUB + fs) * NC + fc] = f * vs;
-            }
-            M = mn;
-          }
           if (tile == pc.first) {  // the next piece's query rows, ahead of their first use
             nx = pc;
             more = nx.next(p);
@@ -616,26 +684,29 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
 #pragma unroll
           for (int h = 0; h < H; ++h)
 #pragma unroll
-            for (int c = 0; c < NC; ++c) e_prev[h][c] = e[h][c];
+            for (int c = 0; c < NP; ++c) e_prev[h][c] = tc::f2_pack(e[h][2 * c], e[h][2 * c + 1]);
           edge_prev = edge;
           edge_n = max(min(pc.nv - t0, TILE_T) - edge, 0);
         }
-        softmax_sync();
+        tile_sync();
         absorb(j - 1);
 
         const size_t slot = (size_t)blockIdx.x + unit;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          float v = l[c];
+          float v0, v1, a0, a1;
+          tc::f2_unpack(l[c / 2], v0, v1);
+          tc::f2_unpack(acc[c / 2], a0, a1);
+          float v = c % 2 ? v1 : v0;
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
           if (lane == 0) smax[warp * NC + c] = v;
-          if (c < p.cols && tid < D) p.part_o[(slot * p.cols + c) * D + tid] = acc[c];
+          if (c < p.cols && tid < D) p.part_o[(slot * p.cols + c) * D + tid] = c % 2 ? a1 : a0;
         }
         softmax_sync();
-        if (tid < p.cols)  // warp 0, lanes of block 0
+        if (tid < p.cols)
           reinterpret_cast<float2*>(p.part_ml)[slot * p.cols + tid] =
-              make_float2(M, (smax[tid] + smax[NC + tid]) + (smax[2 * NC + tid] + smax[3 * NC + tid]));
+              make_float2(fmax_row[tid], (smax[tid] + smax[NC + tid]) + (smax[2 * NC + tid] + smax[3 * NC + tid]));
         if (!more) break;
         pc = nx;
         ++piece;
