@@ -72,7 +72,7 @@ struct Lay {
   static constexpr uint32_t OFF_BAR = OFF_QF + 2 * NC * 4;
   static constexpr int B0 = NK + NV, NBAR = B0 + 9;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr uint32_t BYTES = OFF_MISC + 64 + 1024;
+  static constexpr uint32_t BYTES = OFF_MISC + 128 + 1024;
   // TMEM columns: S two buffers of H parts, O two buffers of SUB parts
   static constexpr uint32_t COL_O = 2 * H * N, COLS_USED = COL_O + 2 * SUB * N;
   static constexpr uint32_t TMEM = COLS_USED <= 64 ? 64 : (COLS_USED <= 128 ? 128 : 256);
@@ -260,6 +260,10 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
   int* sched = reinterpret_cast<int*>(sm + L::OFF_MISC);  // first sequence, its tiles before the share, the
                                                           // share's tiles, the sequence's visible tokens
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::OFF_MISC + 28);
+  // The piece after the present one, [2][6]: whether there is one, b, g, nv, first, last.  Warp 4 alone reads the
+  // lengths for it: the warps that meet at tile_sync have to agree on the pieces even if the lengths changed under
+  // the call.
+  int* follow = reinterpret_cast<int*>(sm + L::OFF_MISC + 64);
   Ctx cx;
   cx.bars = sb + L::OFF_BAR;
   cx.abort_flag = reinterpret_cast<volatile int*>(sm + L::OFF_MISC + 32);
@@ -329,9 +333,20 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
           if (i < NV) load_v();
         }
       }
-      uint32_t j = 0;
+      uint32_t j = 0, piece = 0;
       for (;;) {
         const int blk0 = (pc.b * p.Hkv + pc.g) * p.nblk;
+        Pieces<TILE_T> nx = pc;
+        const bool more = nx.next(p);
+        if (lane == 0) {
+          int* f = follow + (piece & 1) * 6;
+          f[0] = more;
+          f[1] = nx.b;
+          f[2] = nx.g;
+          f[3] = nx.nv;
+          f[4] = nx.first;
+          f[5] = nx.last;
+        }
         float vs_next = 0.f, M = -INFINITY;  // M: running maximum of row fc
         auto load_scale = [&](int tile) {
           const int t = tile * TILE_T + fs * T;
@@ -369,7 +384,9 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
           __syncwarp();
         }
         tile_sync();
-        if (!pc.next(p)) break;
+        if (!more) break;
+        pc = nx;
+        ++piece;
       }
       if (lane == 0 && *cx.abort_flag) {  // every copy that was started lands before the CTA exits
         for (uint32_t i = nk > NK ? nk - NK : 0; i < nk; ++i) drain(cx.bar(L::kf(i % NK)), (i / NK) & 1);
@@ -448,8 +465,7 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
       write_q<D, NC, T>(p, sm, 0, pc.b * p.Hkv + pc.g, tid);
       tc::fence_proxy_async_smem();
       tc::mbar_arrive(cx.bar(L::qf(0)));
-      Pieces<TILE_T> nx = pc;
-      bool more;
+      bool more = false;
       for (;;) {
         const int unit = pc.b * p.Hkv + pc.g;
         const int blk0 = unit * p.nblk;  // B Hkv blocks stay under 2^31
@@ -671,10 +687,10 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
           tc::tc_fence_before();
           tc::mbar_arrive(cx.bar(L::pf(j & 1)));
           if (tile == pc.first) {  // the next piece's query rows, ahead of their first use
-            nx = pc;
-            more = nx.next(p);
+            const int* f = follow + (piece & 1) * 6;
+            more = f[0] != 0;
             if (more) {
-              write_q<D, NC, T>(p, sm, (piece + 1) & 1, nx.b * p.Hkv + nx.g, tid);
+              write_q<D, NC, T>(p, sm, (piece + 1) & 1, f[1] * p.Hkv + f[2], tid);
               tc::fence_proxy_async_smem();
               tc::mbar_arrive(cx.bar(L::qf((piece + 1) & 1)));
             }
@@ -708,7 +724,12 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
           reinterpret_cast<float2*>(p.part_ml)[slot * p.cols + tid] =
               make_float2(fmax_row[tid], (smax[tid] + smax[NC + tid]) + (smax[2 * NC + tid] + smax[3 * NC + tid]));
         if (!more) break;
-        pc = nx;
+        const int* f = follow + (piece & 1) * 6;
+        pc.b = f[1];
+        pc.g = f[2];
+        pc.nv = f[3];
+        pc.first = f[4];
+        pc.last = f[5];
         ++piece;
       }
     }

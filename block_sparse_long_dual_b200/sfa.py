@@ -622,8 +622,10 @@ class FasaDecode:
     calibration that finds them is not part of this library).  Buffers are allocated once;
     ``refresh_keys`` (re)builds the compact key copy for a position range, ``__call__`` runs
     the step's three kernels.  Wherever a key (and value) cache is taken, a ``KvCache8`` of
-    capacity ``seq_len`` may be given instead as ``K_cache`` (``V_cache`` left None): the
-    compact copy and the attention then read the 8-bit cache."""
+    capacity ``seq_len`` that holds ``seq_len`` tokens may be given instead as ``K_cache``
+    (``V_cache`` left None): the compact copy and the attention then read the 8-bit cache.  (The
+    selection ranks all ``seq_len`` rows; a row that picks one behind ``lens`` is reported in
+    ``status`` as SFA_ERR_INDEX and comes out 0.)"""
 
     def __init__(self, *, batch, heads_q, heads_kv, seq_len, head_dim, fc, k, device="cuda", with_lse=True):
         self.fc = fc
@@ -702,6 +704,13 @@ def _fits(t, name, shape, dtype, device):
     if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         _expect(t, name, shape, dtype, device)
     return t.data_ptr()
+
+
+def _fresh(t, stream):
+    """A buffer allocated for a call on ``stream``: its memory is not reused before that stream is done with it."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
 
 
 class KvCache8:
@@ -847,11 +856,11 @@ def cache8_attn(q, cache: KvCache8, *, back: int = 0, scale: float = 0.0, o=None
     shape, nq = _cache8_query(q, cache)
     dev, st = cache._launch(stream)
     sizes = q.shape
-    o = torch.empty_like(q) if o is None else o
+    o = _fresh(torch.empty_like(q), stream) if o is None else o
     tokens = (cache.batch, cache.heads_kv, cache.capacity)
     if workspace is None:
-        workspace = torch.empty(cache8_attn_workspace(q, cache, weights=weight_out is not None), dtype=torch.uint8,
-                                device=dev)
+        workspace = _fresh(torch.empty(cache8_attn_workspace(q, cache, weights=weight_out is not None),
+                                       dtype=torch.uint8, device=dev), stream)
     nbytes = workspace.numel()
     _check(lib.sfa_cache8_attn(shape, cache._cref, _fits(q, "q", sizes, torch.bfloat16, dev), nq, back, scale,
                                _fits(o, "o", sizes, torch.bfloat16, dev),
@@ -870,7 +879,7 @@ def cache8_attn_list(q, cache: KvCache8, idx, *, scale: float = 0.0, o=None, lse
         raise ValueError("q must be [B, Hq, d] and idx [B, Hq, k]")
     shape, _ = _cache8_query(q, cache)
     dev, st = cache._launch(stream)
-    o = torch.empty_like(q) if o is None else o
+    o = _fresh(torch.empty_like(q), stream) if o is None else o
     rows, k = q.shape[:2], idx.shape[2]
     _check(lib.sfa_cache8_attn_list(shape, cache._cref, _fits(q, "q", q.shape, torch.bfloat16, dev),
                                     _fits(idx, "idx", (*rows, k), torch.int32, dev), k, scale,
@@ -899,7 +908,7 @@ def cache8_evict(src: KvCache8, dst: KvCache8, *, keep: int, recent: int = 0, id
     if dst.k.device != dev:
         raise ValueError(f"dst must be on {dev}, got {dst.k.device}")
     if idx is None:
-        idx = torch.empty((src.batch, src.heads_kv, max(int(keep), 0)), dtype=torch.int32, device=dev)
+        idx = _fresh(torch.empty((src.batch, src.heads_kv, max(int(keep), 0)), dtype=torch.int32, device=dev), stream)
     nbytes = 0 if workspace is None else workspace.numel()
     _check(lib.sfa_cache8_evict(src._kv_ref, src._cref, dst._cref, dst.capacity, keep, recent,
                                 _fits(idx, "idx", (src.batch, src.heads_kv, keep), torch.int32, dev),
@@ -918,7 +927,7 @@ def cache8_fc_gather(cache: KvCache8, fc, *, K_fc=None, pos0: int = 0, npos: int
     nfc = pairs.shape[1]
     dev, st = cache._launch(stream)
     rows = (cache.batch, cache.heads_kv, cache.capacity, 2 * nfc)
-    K_fc = torch.empty(rows, dtype=torch.bfloat16, device=dev) if K_fc is None else K_fc
+    K_fc = _fresh(torch.empty(rows, dtype=torch.bfloat16, device=dev), stream) if K_fc is None else K_fc
     npos = cache.capacity - pos0 if npos is None else npos
     _check(lib.sfa_cache8_fc_gather(cache._kv_ref, cache._cref, pairs.ctypes.data, nfc, pos0, npos,
                                     _fits(K_fc, "K_fc", rows, torch.bfloat16, dev), st), "sfa_cache8_fc_gather")

@@ -358,6 +358,8 @@ sfa_status sfa_decode_attn(const sfa_shape* shape, const void* q, const void* K_
  *   weight            [B, heads_kv, L] float32: attention weight each token has
  *                     received so far (may be NULL where a call does not use it)
  * Rows at and after lens[b] are never read into a result and may hold anything.
+ * lens and the other arrays must not change while a call's kernels run (calls on
+ * one stream follow each other; order calls on several yourself).
  * Shape rules: those of the decode calls above (dtype SFA_BF16; d in {64, 128};
  * heads_q / heads_kv in {1, 2, 4, 8}; batch * heads_kv * L < 2^31), block in
  * {64, 128} (SFA_ERR_SHAPE); any L >= 1.  A length or position found out of

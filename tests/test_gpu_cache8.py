@@ -201,6 +201,12 @@ ATTNS = [  # B, Hkv, G, cap, d, block, nq, back, lens, spread
     (2, 2, 4, 600, 128, 64, 1, 0, (600, 333), 6),     # scales far apart between blocks
     (2, 2, 4, 600, 64, 128, 3, 0, (600, 333), 6),
     (9, 8, 4, 900, 128, 128, 1, 0, (900, 1, 2, 3, 500, 0, 700, 800, 31), 1),  # pieces that cross sequences
+    (1, 1, 1, 1, 64, 64, 1, 0, (1,), 0),
+    (2, 2, 8, 700, 64, 64, 2, 3, (700, 2), 2),        # 16 rows, small blocks
+    (1, 2, 1, 600, 64, 128, 11, 0, (600,), 1),        # 11 rows: padded to 12
+    (20, 8, 4, 200, 128, 64, 1, 0, tuple(range(0, 200, 10)), 0),   # more rows than joining CTAs fit at once
+    (3, 1, 1, 300, 128, 128, 16, 0, (300, 15, 256), 0),
+    (4, 2, 2, 50, 64, 64, 1, 0, (0, 0, 0, 0), 0),     # nothing anywhere
 ]
 
 
@@ -390,6 +396,7 @@ LISTS = [  # B, Hkv, G, cap, d, block, k, lens
     (3, 1, 8, 700, 64, 64, 77, (700, 0, 5)),
     (2, 2, 2, 900, 128, 64, 1023, (900, 899)),
     (40, 8, 1, 130, 128, 128, 33, tuple(range(1, 41))),
+    (1, 1, 2, 5000, 64, 128, 4500, (5000,)),   # a list staged in parts
 ]
 
 
@@ -499,6 +506,47 @@ def test_compact_keys(nfc, d):
     want = np.full(out.shape, 7.0)
     want[:, :, 60:261] = co.fc_gather(arr.k, arr.ks, fc, 64)[:, :, 60:261]
     np.testing.assert_array_equal(out.double().cpu().numpy(), want)
+
+
+def test_offsets_beyond_32_bits():
+    """Twelve heads of 2 million tokens (3 GB of keys, as much of values): rows at the end of the last head.  All
+    tokens but the last 300 are zero, so the softmax has a closed form."""
+    n, cap, m = 1_999_990, 2_000_000, 300
+    rng = np.random.default_rng(51)
+    cache = sfa.KvCache8.empty(batch=1, heads_kv=12, capacity=cap, head_dim=128)
+    K, V = (bf16(rng.normal(size=(1, 12, m, 128))) for _ in range(2))
+    cache.append(K.to(dev()), V.to(dev()), at=i32([n - m]))
+    assert cache.lens.tolist() == [n]
+    tail = slice((n - m) // 128 * 128, cap)
+    held = [codes(x[:, 11:, tail]) for x in (cache.k, cache.v)] + [x[0, 11, tail.start // 128:].cpu().numpy()
+                                                                 for x in (cache.k_scale, cache.v_scale)]
+    off = n - m - tail.start
+    k = co.values(held[0][0, 0], held[2], 128)[off: off + m]
+    v = co.values(held[1][0, 0], held[3], 128)[off: off + m]
+    close(torch.from_numpy(k), K[0, 11].double().numpy(), 2.0 ** -4 * np.abs(K[0, 11].double().numpy()) + 2.0 ** -10, "k")
+    q = bf16(rng.normal(size=(1, 12, 128)) * 3)
+    lse = torch.empty((1, 12), device=dev())
+    o = cache.attend(q.to(dev()), accumulate=True, lse=lse)
+    e = np.exp(k @ q[0, 11].double().numpy() / 128 ** 0.5)
+    z = e.sum() + n - m
+    assert abs(lse[0, 11].item() - np.log(z)) < 1e-5
+    # a probability's two parts end 2^-23 under its block's largest; sums of 300 terms
+    tol = (2.0 ** -8 + 2.0 ** -12) * (e @ np.abs(v)) / z + 2.0 ** -22 * e.max() / z * np.abs(v).sum(0) + 2.0 ** -30
+    assert np.all(np.abs(o[0, 11].double().cpu().numpy() - e @ v / z) <= tol + 2.0 ** -8 * np.abs(e @ v / z))
+    idx = torch.arange(n - m, n, dtype=torch.int32, device=dev()).expand(1, 12, m).contiguous()
+    ol = cache.attend_list(q.to(dev()), idx)
+    np.testing.assert_allclose(ol[0, 11].double().cpu().numpy(), e @ v / e.sum(), rtol=2e-2, atol=1e-2)
+    fc = np.tile(np.arange(4), (12, 1))
+    K_fc = sfa.cache8_fc_gather(cache, fc, pos0=n - m, npos=m)
+    np.testing.assert_array_equal(K_fc[0, 11, n - m:n].double().cpu().numpy(), k[:, [0, 1, 2, 3, 64, 65, 66, 67]])
+    cache.weight[0, 11, n - m] = 5.0
+    small = sfa.KvCache8.empty(batch=1, heads_kv=12, capacity=128, head_dim=128)
+    kept = cache.evict(small, keep=100, recent=99)
+    assert kept[0, 11].tolist() == [n - m] + list(range(n - 99, n))
+    got = co.values(codes(small.k)[0, 11], small.k_scale[0, 11].cpu().numpy(), 128)[:100]
+    want = k[[0] + list(range(m - 99, m))]
+    assert np.all(np.abs(got - want) <= 2.0 ** -4 * np.abs(want) + 2.0 ** -9)
+    assert int(cache.status.item()) == 0
 
 
 # ---------------------------------------------------------------------------
