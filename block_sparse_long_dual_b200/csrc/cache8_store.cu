@@ -132,14 +132,11 @@ __global__ void advance_kernel(Cache8Append p) {
 // bits, so neighbouring lanes would queue on one bin: two copies of the histogram,
 // sixteen banks apart.
 // ---------------------------------------------------------------------------
-constexpr int kSelThreads = 1024;
 constexpr int kSlice = 16384;  // keys in shared memory
 constexpr int kBins = 2048, kBinStride = kBins + 16;
-constexpr int kBpt = kBins / kSelThreads;  // bins per thread
-constexpr int kPerThread = kSlice / kSelThreads;
-// One word of padding per thread's 16 consecutive keys: both orders of access spread over the banks.
-__device__ __forceinline__ int key_at(int i) { return i + i / kPerThread; }
-constexpr int kKeyWords = kSlice + kSelThreads;
+// One word of padding per 32 keys: neighbouring keys and keys a small power of two apart spread over the banks.
+__device__ __forceinline__ int key_at(int i) { return i + (i >> 5); }
+constexpr int kKeyWords = kSlice + kSlice / 32;
 constexpr size_t kSelSmem = ((size_t)kKeyWords + 2 * kBinStride) * sizeof(uint32_t);
 
 // Exclusive sum over the block of a 32-bit value.
@@ -157,12 +154,13 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* wsum) {
   return __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0u) + inc - x;
 }
 
-template <int CS>
+template <int CS, int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __grid_constant__ Cache8Evict p) {
+  constexpr int kBpt = kBins / kSelThreads;  // bins per thread
   extern __shared__ __align__(16) uint32_t sel_smem[];
   uint32_t* key = sel_smem;                // [kKeyWords], through key_at
   uint32_t* hist = sel_smem + kKeyWords;   // [2][kBinStride]
-  __shared__ uint32_t fold[2][CS > 1 ? kBins : 1];  // this slice's bins (two: a pass may begin while others read)
+  __shared__ __align__(16) uint32_t fold[2][CS > 1 ? kBins : 2];  // this slice's bins (two: a pass may begin while others read)
   __shared__ uint32_t part[2][CS > 1 ? kBins / CS : 1], ptotal[2];  // this CTA's share of the bins, over all slices
   __shared__ uint32_t wsum[kSelThreads / 32];
   __shared__ uint32_t share[2];  // this slice's keys above and at the threshold
@@ -219,21 +217,24 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
       }
     }
     __syncthreads();
-    // Thread t owns the bins [2 t', 2 t' + 2), t' = 1023 - t: an exclusive sum over t runs from the top bin down.
+    // Thread t owns the kBpt bins from bin0 on, the first thread the top ones: an exclusive sum over t runs from the
+    // top bin down.
     const int bin0 = kBins - kBpt * (tid + 1);
-    uint32_t own[kBpt] = {0, 0};
+    uint32_t own[kBpt];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint2* h = reinterpret_cast<uint2*>(hist + q * kBinStride + bin0);
-      const uint2 u = *h;
-      own[0] += u.x;
-      own[1] += u.y;
-      *h = make_uint2(0, 0);
+    for (int j = 0; j < kBpt; j += 2) {
+      uint2* h = reinterpret_cast<uint2*>(hist + bin0 + j);
+      uint2* g = reinterpret_cast<uint2*>(hist + kBinStride + bin0 + j);
+      const uint2 u = *h, v = *g;
+      own[j] = u.x + v.x;
+      own[j + 1] = u.y + v.y;
+      *h = *g = make_uint2(0, 0);
     }
     if (CS > 1) {
       constexpr int PB = kBins / CS;
       uint32_t *mine = fold[pass & 1], *sum = part[pass & 1];
-      *reinterpret_cast<uint2*>(mine + bin0) = make_uint2(own[0], own[1]);
+#pragma unroll
+      for (int j = 0; j < kBpt; j += 2) *reinterpret_cast<uint2*>(mine + bin0 + j) = make_uint2(own[j], own[j + 1]);
       if (tid == 0) ptotal[pass & 1] = 0;
       cluster.sync();
       if (tid < PB) {
@@ -265,7 +266,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
         sh_above = before;
       }
     } else {
-      uint32_t before = block_scan(own[0] + own[1], wsum);
+      uint32_t all = 0;
+#pragma unroll
+      for (int j = 0; j < kBpt; ++j) all += own[j];
+      uint32_t before = block_scan(all, wsum);
 #pragma unroll
       for (int j = kBpt - 1; j >= 0; --j) {
         if (before < need && before + own[j] >= need) {
@@ -302,26 +306,29 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
   }
   for (int from = lo; from < hi; from += kSlice) {
     if (!whole) load(from);
-    const uint32_t* mine = key + tid * (kPerThread + 1);  // the keys [16 tid, 16 tid + 16)
-    const int have = min(kPerThread, cnt - tid * kPerThread);
+    const int span = (cnt + kSelThreads - 1) / kSelThreads;  // this thread: the keys [k0, k1)
+    const int k0 = min(tid * span, cnt), k1 = min(k0 + span, cnt);
     uint32_t pk = 0;  // (greater << 16) | equal: 16384 keys at most
 #pragma unroll 4
-    for (int j = 0; j < have; ++j) pk += mine[j] > prefix ? 65536u : (mine[j] == prefix ? 1u : 0u);
+    for (int i = k0; i < k1; ++i) {
+      const uint32_t k = key[key_at(i)];
+      pk += k > prefix ? 65536u : (k == prefix ? 1u : 0u);
+    }
     const uint32_t before = block_scan(pk, wsum);
     uint32_t g = gt + (before >> 16), e = eq + (before & 0xFFFFu);
     if (pk != 0) {
 #pragma unroll 4
-      for (int j = 0; j < have; ++j) {
-        const uint32_t k = mine[j];
+      for (int i = k0; i < k1; ++i) {
+        const uint32_t k = key[key_at(i)];
         if (k >= prefix) {
-          if (k > prefix || e < need) out[g + min(e, need)] = first + tid * kPerThread + j;
+          if (k > prefix || e < need) out[g + min(e, need)] = first + i;
           g += k > prefix;
           e += k == prefix;
         }
       }
     }
     if (!whole) {  // wsum still holds the warps' totals
-      const uint32_t all = __reduce_add_sync(0xffffffffu, wsum[lane]);
+      const uint32_t all = __reduce_add_sync(0xffffffffu, lane < kSelThreads / 32 ? wsum[lane] : 0u);
       gt += all >> 16;
       eq += all & 0xFFFFu;
     }
@@ -329,10 +336,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
   if (CS > 1) cluster.sync();  // the other CTAs have read this one's shared memory
 }
 
-template <int CS>
+template <int CS, int kSelThreads>
 static cudaError_t launch_select(const Cache8Evict& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem_once(evict_select_kernel<CS>, kSelSmem, false, done);
+  const cudaError_t e = allow_smem_once(evict_select_kernel<CS, kSelThreads>, kSelSmem, false, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.dynamicSmemBytes = kSelSmem;
@@ -345,7 +352,7 @@ static cudaError_t launch_select(const Cache8Evict& p, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = CS > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<CS>, p);
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<CS, kSelThreads>, p);
 }
 
 // evict, move: a CTA per (dst block, (b, KV head), K or V), eight to an SM (two dependent loads, a reduction and a
@@ -487,8 +494,9 @@ cudaError_t launch_cache8_append(const Cache8Append& p, cudaStream_t st) {
 
 cudaError_t launch_cache8_evict(const Cache8Evict& p, cudaStream_t st) {
   if ((long long)p.B * p.Hkv * 8 >= (1LL << 31)) return cudaErrorInvalidValue;
-  // One CTA's shared memory holds 16384 keys; longer caches are spread over eight CTAs a head.
-  cudaError_t e = p.L > kSlice ? launch_select<8>(p, st) : launch_select<1>(p, st);
+  // One CTA's shared memory holds 16384 keys; longer caches are spread over eight CTAs a head, of half the threads
+  // (two share an SM, and every warp pays for the meetings: 131072 tokens 32 against 40 us).
+  cudaError_t e = p.L > kSlice ? launch_select<8, 512>(p, st) : launch_select<1, 1024>(p, st);
   if (e != cudaSuccess) return e;
   const int most = p.keep < p.L ? p.keep : p.L;
   const int nb = (most + p.T - 1) / p.T;
