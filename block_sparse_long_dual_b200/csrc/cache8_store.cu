@@ -3,6 +3,7 @@
 #include <cooperative_groups.h>
 
 #include "cache8.cuh"
+#include "tc_ptx.cuh"
 
 namespace sfa {
 
@@ -66,16 +67,27 @@ __global__ void __launch_bounds__(kAppend, 4) append_kernel(Cache8Append p, int 
       x[c] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)(row - at) * D + (i % CPR) * 8));
   }
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = (w[e] & 0x7FFFu) << 16, hi = w[e] & 0x7FFF0000u;
-      if (lo < 0x7F800000u) top = max(top, lo);
-      if (hi < 0x7F800000u) top = max(top, hi);
-    }
+  for (int c = 0; c < CH; ++c) {  // bf16 magnitudes order like their bits: two at a time
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[c].x & 0x7FFF7FFFu, x[c].y & 0x7FFF7FFFu),
+                                 __vmaxu2(x[c].z & 0x7FFF7FFFu, x[c].w & 0x7FFF7FFFu)));
   }
-  top = block_max<kAppend>(top, sh);
+  top = block_max<kAppend>(max(top & 0xFFFFu, top >> 16), sh);
+  const bool finite = top < 0x7F80u;
+  if (!finite) {  // an infinity or NaN somewhere in the block: the largest of the others
+    top = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
+        top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+      }
+    }
+    __syncthreads();  // sh has been read
+    top = block_max<kAppend>(top, sh);
+  }
+  top <<= 16;
   int ex = need_exp(top);
   const bool grown = row0 < at && ex > was;
   if (row0 < at && was > ex) ex = was;
@@ -84,14 +96,25 @@ __global__ void __launch_bounds__(kAppend, 4) append_kernel(Cache8Append p, int 
   for (int c = 0; c < CH; ++c) {
     const int i = tid + c * kAppend, row = row0 + i / CPR;
     if (row >= at && row < end) {
-      const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+      uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
       uint32_t o[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xFFFF0000u);
-        o[e] = to_e4m3x2(isfinite(lo) ? lo * inv : NAN, isfinite(hi) ? hi * inv : NAN);
+        uint64_t v = tc::f2_mul(tc::f2_pack(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)),
+                                tc::f2_pack(inv, inv));
+        float lo, hi;
+        tc::f2_unpack(v, lo, hi);
+        o[e] = to_e4m3x2(lo, hi);
       }
-      *reinterpret_cast<uint2*>(dst + (size_t)i * 8) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+      if (!finite) {  // infinities (that the conversion would saturate) become NaN like NaN itself
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if ((w[e] & 0x7FFFu) >= 0x7F80u) o[e] = (o[e] & 0xFF00u) | 0x7Fu;
+          if ((w[e] & 0x7FFF0000u) >= 0x7F800000u) o[e] = (o[e] & 0xFFu) | 0x7F00u;
+        }
+      }
+      *reinterpret_cast<uint2*>(dst + (size_t)i * 8) =
+          make_uint2(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410));
     } else if (grown && row < at) {  // earlier rows of the block move to the larger scale
       uint2* cp = reinterpret_cast<uint2*>(dst + (size_t)i * 8);
       const uint2 u = *cp;
@@ -386,17 +409,25 @@ __global__ void __launch_bounds__(kThreads, 8) evict_move_kernel(const __grid_co
       ex[c] = scale_exp(__ldg(scale + at[c] / T));
     }
   }
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+  // The largest magnitude of the chunk's 16 codes, two bytes a word at a time; 0x7F is NaN, which does not count.
+  auto top_code = [](const uint4& u, bool skip_nan) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t a = w[e] & 0x7F7F7F7Fu;
-      m = __vmaxu4(m, a & ~__vcmpeq4(a, 0x7F7F7F7Fu));  // NaN codes do not count
+      uint32_t a = w[e] & 0x007F007Fu, d = (w[e] >> 8) & 0x007F007Fu;
+      if (skip_nan) {
+        a &= ~__vcmpeq2(a, 0x007F007Fu);
+        d &= ~__vcmpeq2(d, 0x007F007Fu);
+      }
+      m = __vmaxu2(m, __vmaxu2(a, d));
     }
-    m = __vmaxu4(m, m >> 16);
-    m = __vmaxu4(m, m >> 8) & 0x7Fu;
+    return max(m & 0xFFFFu, m >> 16);
+  };
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    uint32_t m = top_code(x[c], false);
+    if (m == 0x7Fu) m = top_code(x[c], true);
     if (m != 0) need = max(need, need_exp(__float_as_uint(__half2float(__low2half(from_e4m3x2(m))))) + ex[c]);
   }
   need = (int)block_max<kThreads>((uint32_t)(need - kMinExp), sh) + kMinExp;
@@ -456,17 +487,16 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   }
   __syncthreads();
   uint32_t* out = reinterpret_cast<uint32_t*>(p.out) + ((size_t)unit * p.L + t0) * p.nfc;
-  const int step_r = kThreads / p.nfc, step_w = kThreads % p.nfc;
-  int r = tid / p.nfc, w = tid % p.nfc;
-  const uint8_t* bytes = reinterpret_cast<const uint8_t*>(rows);
-  for (int i = tid; i < n * p.nfc; i += kThreads) {
-    const uint32_t at = pair[w];
-    const uint8_t* row = bytes + r * STRIDE;
-    const float2 v = __half22float2(from_e4m3x2(row[at & 255u] | ((uint32_t)row[at >> 8] << 8)));
-    out[i] = pack_bf16x2(v.x * sc[r], v.y * sc[r]);
-    r += step_r;
-    w += step_w;
-    if (w >= p.nfc) { w -= p.nfc; ++r; }
+  const int per = kThreads / p.nfc;  // tokens the CTA writes at a time; a thread keeps its column pair
+  const int r0 = tid / p.nfc, w = tid % p.nfc;
+  if (r0 >= per) return;
+  const uint8_t* lo = reinterpret_cast<const uint8_t*>(rows) + (pair[w] & 255u);
+  const uint8_t* hi = reinterpret_cast<const uint8_t*>(rows) + (pair[w] >> 8);
+#pragma unroll 4
+  for (int r = r0; r < n; r += per) {
+    const float2 v = __half22float2(from_e4m3x2(lo[r * STRIDE] | ((uint32_t)hi[r * STRIDE] << 8)));
+    const float f = sc[r];
+    out[r * p.nfc + w] = pack_bf16x2(v.x * f, v.y * f);
   }
 }
 
