@@ -421,7 +421,9 @@ size_t sfa_cache8_attn_workspace(const sfa_shape* shape, int nq, int weights);
  * A q element that is NaN or infinite makes its row's o NaN.
  * workspace: device, at least sfa_cache8_attn_workspace() bytes, 256-byte
  * aligned; nothing in it is kept between calls, and calls whose kernels overlap
- * on the GPU need one each.  A length outside [0, L] counts as 0.
+ * on the GPU need one each.  A length outside [0, L] counts as 0.  A wait inside
+ * the kernel that runs out (about 2 s) sets SFA_ERR_TIMEOUT; the outputs are then
+ * not valid.  Launches 2 kernels.
  */
 sfa_status sfa_cache8_attn(const sfa_shape* shape, const sfa_cache8* cache, const void* q, int nq,
                            int back, float scale, void* o, float* lse, const float* weight_in,
