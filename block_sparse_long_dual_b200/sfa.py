@@ -706,6 +706,10 @@ def _fits(t, name, shape, dtype, device):
     return t.data_ptr()
 
 
+def _handle(stream):
+    return stream.value if isinstance(stream, c_void_p) else stream
+
+
 def _fresh(t, stream):
     """A buffer allocated for a call on ``stream``: its memory is not reused before that stream is done with it."""
     if stream is not None:
@@ -784,12 +788,15 @@ class KvCache8:
             _status(status)
         return status.data_ptr()
 
-    def _workspace(self, q, weights):
-        """The handle's own attention workspace for queries like q (one per shape, made on first use)."""
-        key = (q.shape[1], q.shape[2] if q.dim() == 4 else 1, weights)
+    def _workspace(self, q, weights, stream):
+        """The handle's own attention workspace for queries like q on one stream (made on first use).  None while a
+        graph is captured: the call then takes one from that graph's pool, so that no two graphs share it."""
+        if torch.cuda.is_current_stream_capturing():
+            return None
+        key = (q.shape[1], q.shape[2] if q.dim() == 4 else 1, weights, _handle(self._launch(stream)[1]))
         if key not in self._workspaces:
-            self._workspaces[key] = torch.empty(cache8_attn_workspace(q, self, weights=weights), dtype=torch.uint8,
-                                                device=self.k.device)
+            self._workspaces[key] = _fresh(torch.empty(cache8_attn_workspace(q, self, weights=weights),
+                                                       dtype=torch.uint8, device=self.k.device), stream)
         return self._workspaces[key]
 
     def append(self, K, V, *, at=None, counts=None, stream=None):
@@ -798,13 +805,13 @@ class KvCache8:
 
     def attend(self, q, *, back=0, scale=0.0, accumulate=False, o=None, lse=None, stream=None):
         """Attention of q [B, Hq, d] or [B, Hq, nq, d] over the whole cache; ``accumulate`` adds the
-        attention weights to ``weight``.  Uses the handle's workspace: calls that overlap on the GPU (other
-        streams, captured graphs replayed together) need cache8_attn with a workspace each."""
+        attention weights to ``weight`` (calls that do so follow each other: order streams yourself).
+        The handle keeps a workspace per stream."""
         if accumulate and self.weight is None:
             raise ValueError("accumulate needs a cache with weights")
         w = self.weight if accumulate else None
         return cache8_attn(q, self, back=back, scale=scale, o=o, lse=lse, weight_in=w, weight_out=w,
-                           workspace=self._workspace(q, accumulate), status=self.status, stream=stream)
+                           workspace=self._workspace(q, accumulate, stream), status=self.status, stream=stream)
 
     def attend_list(self, q, idx, *, scale=0.0, o=None, lse=None, stream=None):
         """Attention of q [B, Hq, d] over the tokens of idx [B, Hq, k]; see cache8_attn_list."""

@@ -329,7 +329,6 @@ def test_attention_in_a_graph_follows_the_lengths():
     with torch.cuda.stream(side):
         scratch.append(K, V)
         scratch.attend(q, accumulate=True)
-        cache._workspace(q, True)
     torch.cuda.current_stream().wait_stream(side)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
@@ -359,6 +358,35 @@ def test_two_streams_with_a_workspace_each():
     for _ in range(10):
         for q, w, o, s in zip(qs, ws, outs, streams):
             sfa.cache8_attn(q, cache, workspace=w, o=o, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+    for _ in range(10):  # the handle's own workspaces: one a stream
+        got = [cache.attend(q, o=o, stream=s) for q, o, s in zip(qs, outs, streams)]
+    torch.cuda.synchronize()
+    for o, w in zip(got, want):
+        assert torch.equal(o, w)
+
+
+def test_two_graphs_of_one_cache_replayed_together():
+    """Each captured attention has a workspace of its own, although the handle is shared."""
+    rng = np.random.default_rng(18)
+    arr = Arrays(rng, 2, 2, 6000, 128, 64, (6000, 3000))
+    cache = arr.gpu()
+    qs = [bf16(rng.normal(size=(2, 8, 128))).to(dev()) for _ in range(2)]
+    want = [cache.attend(q) for q in qs]
+    outs, graphs, streams = [torch.empty_like(q) for q in qs], [], [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for q, o in zip(qs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(5):
+                cache.attend(q, o=o)
+        graphs.append(g)
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert torch.equal(o, w)
