@@ -27,8 +27,9 @@ constexpr int kJoinThreads = 256;
 
 __device__ __forceinline__ void pieces_ready() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Tokens per thread of the weights part: about eight 16-byte loads of scores in flight.
-constexpr int weight_tokens(int CP) { return CP <= 4 ? 8 : (CP == 8 ? 4 : 2); }
+// Tokens per thread of the weights part: about four 16-byte loads of scores in flight (128K x 4 with weights: the
+// whole call 201.5 us, 204.5 with eight, which spill).
+constexpr int weight_tokens(int CP) { return CP <= 4 ? 4 : (CP == 8 ? 2 : 1); }
 
 template <int D, int CP, bool UNIT>  // CP = p.cpad; UNIT: a joining CTA takes all rows of a unit
 __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid_constant__ Cache8Attn p, int parts,
@@ -187,11 +188,12 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
 
 template <int D, int CP, bool UNIT>
 static cudaError_t launch_join(const Cache8Attn& p, cudaStream_t st) {
-  // The weights part: CTAs of whole chunks, about four CTAs per SM in all (each pays its start once).
+  // The weights part: CTAs of whole chunks, as many as are resident beside the joining ones (each pays its start once).
   const int chunk = weight_tokens(CP) * kJoinThreads, chunks = (p.L + chunk - 1) / chunk;
-  const long long units = (long long)p.B * p.Hkv;
-  long long each = units * chunks / (4 * kSms);
-  each = each < 1 ? 1 : (each > chunks ? chunks : each);
+  const long long units = (long long)p.B * p.Hkv, joining = units * (UNIT ? 1 : p.cols);
+  const long long room = 4 * kSms - joining > kSms ? 4 * kSms - joining : kSms;
+  long long each = (units * chunks + room - 1) / room;
+  each = each > chunks ? chunks : each;
   const int parts = (int)((chunks + each - 1) / each);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.B * p.Hkv * ((UNIT ? 1 : p.cols) + (p.w_out != nullptr ? parts : 0)));

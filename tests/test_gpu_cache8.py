@@ -207,6 +207,8 @@ ATTNS = [  # B, Hkv, G, cap, d, block, nq, back, lens, spread
     (20, 8, 4, 200, 128, 64, 1, 0, tuple(range(0, 200, 10)), 0),   # more rows than joining CTAs fit at once
     (3, 1, 1, 300, 128, 128, 16, 0, (300, 15, 256), 0),
     (4, 2, 2, 50, 64, 64, 1, 0, (0, 0, 0, 0), 0),     # nothing anywhere
+    (3, 2, 1, 600, 64, 64, 8, 0, (259, 512, 258), 2),  # the causal edge over two tiles of 256
+    (3, 1, 1, 300, 128, 128, 8, 0, (130, 256, 263), 1),  # and of 128
 ]
 
 
