@@ -69,7 +69,8 @@ struct Lay {
   static constexpr uint32_t OFF_FAC = OFF_MAX + 2 * H * 4 * NC * 4;  // [2][NC] keep, [2][SUB][NC] f,
                                                                      // [2][SUB][NC] f v, [NC] running maxima
   static constexpr uint32_t OFF_QF = OFF_FAC + NC * (3 + 4 * SUB) * 4;  // row factors [2][NC]
-  static constexpr uint32_t OFF_BAR = OFF_QF + 2 * NC * 4;
+  static constexpr uint32_t OFF_BACK = OFF_QF + 2 * NC * 4;          // newest tokens that a row does not see [NC]
+  static constexpr uint32_t OFF_BAR = OFF_BACK + NC * 4;
   static constexpr int B0 = NK + NV, NBAR = B0 + 9;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t BYTES = OFF_MISC + 128 + 1024;
@@ -288,6 +289,8 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
     tc::fence_mbar_init();
     tc::prefetch_tmap(&tmK);
     tc::prefetch_tmap(&tmV);
+  } else if (warp == 1) {
+    if (lane < NC) reinterpret_cast<int*>(sm + L::OFF_BACK)[lane] = p.nq - 1 - lane % p.nq;
   } else if (warp == 5) {
     tc::tmem_alloc(tc::smem_u32(tmem_slot), L::TMEM);
     tc::tmem_relinquish();
@@ -457,6 +460,7 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
       const float* fmax_row = ffv + 2 * SUB * NC;                 // [NC]
       float* ee = reinterpret_cast<float*>(sm + L::OFF_EE);       // [2][kEdge][NC]
       const float* qfac = reinterpret_cast<const float*>(sm + L::OFF_QF);
+      const int* unseen = reinterpret_cast<const int*>(sm + L::OFF_BACK);
       const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
       constexpr int WPS = T / 32;  // warps per scale block
       const int my_sub = tid / T;  // scale block of this thread's token within its 128
@@ -539,8 +543,9 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
           }
           for (int r = 0; r < edge_n; ++r) {
             const float v = __low2float(from_e4m3x2(sm[L::OFF_EV + ((i & 1) * kEdge + r) * D + tid % D])) * kTopP;
-            const float* er = ee + ((i & 1) * kEdge + r) * NC;
-            const float* vr = vp + ((edge_prev + r) / T) * NC;
+            float er[NC], vr[NC];
+            load_row<NC>(ee + ((i & 1) * kEdge + r) * NC, er);
+            load_row<NC>(vp + ((edge_prev + r) / T) * NC, vr);
 #pragma unroll
             for (int c = 0; c < NP; ++c) {
               float a0, a1;
@@ -581,14 +586,12 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
             }
           }
           if (edge < TILE_T) {  // only here some row does not see some token; rows from cols on are never used
-            for (int i = 0; i < p.nq; ++i) {
 #pragma unroll
-              for (int h = 0; h < H; ++h) {
-                const bool sees = t0 + h * 128 + tid < pc.nv - (p.nq - 1 - i);
+            for (int c = 0; c < NC; ++c) {
+              const int last = pc.nv - unseen[c] - t0;
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
-                  if (!sees && c % p.nq == i) e[h][c] = -INFINITY;
-              }
+              for (int h = 0; h < H; ++h)
+                if (h * 128 + tid >= last) e[h][c] = -INFINITY;
             }
           }
           float* wm = smax + (j & 1) * H * 4 * NC;
@@ -677,7 +680,7 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
                 for (int k = 0; k < D / 16; ++k) ev[k] = row[k ^ (D == 128 ? (i & 7) : ((i >> 1) & 3))];
                 float* er = ee + ((j & 1) * kEdge + i - edge) * NC;
 #pragma unroll
-                for (int c = 0; c < NC; ++c) er[c] = t < pc.nv - (p.nq - 1 - c % p.nq) ? e[h][c] : -1.f;
+                for (int c = 0; c < NC; ++c) er[c] = t < pc.nv - unseen[c] ? e[h][c] : -1.f;
               }
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) row[k] = make_uint4(0, 0, 0, 0);
