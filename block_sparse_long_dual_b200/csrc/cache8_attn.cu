@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
   }
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   pieces_ready();
+  if (join && np == 1) return;  // one piece: the first step has written the outputs
   if (join && UNIT) {
     const int grp = tid / D, r = tid % D;
     for (int c = grp; c < p.cols; c += GR) {

@@ -176,6 +176,27 @@ __device__ __forceinline__ uint64_t pair_bits(uint32_t a, uint32_t b) {
   return tc::f2_pack(__uint_as_float(a), __uint_as_float(b));
 }
 
+// Sums of NC values over the warp, each lane left with the sum of one row (*row): halves are exchanged, then quarters...
+template <int NC>
+__device__ __forceinline__ float warp_row_sums(float (&x)[NC], int* row) {
+  const int lane = threadIdx.x & 31;
+  int r = 0, m = 16;
+#pragma unroll
+  for (int w = NC / 2; w >= 1; w /= 2, m /= 2) {
+    const bool up = (lane & m) != 0;
+#pragma unroll
+    for (int c = 0; c < w; ++c) {
+      const float give = up ? x[c] : x[c + w], own = up ? x[c + w] : x[c];
+      x[c] = own + __shfl_xor_sync(0xffffffffu, give, m);
+    }
+    r += up ? w : 0;
+  }
+#pragma unroll
+  for (; m >= 1; m /= 2) x[0] += __shfl_xor_sync(0xffffffffu, x[0], m);
+  *row = r;
+  return x[0];
+}
+
 template <int N>
 __device__ __forceinline__ void tmem_row(uint32_t at, uint32_t (&v)[N]) {
   static_assert(N == 16 || N == 32, "two columns a query row");
@@ -710,22 +731,51 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
         tile_sync();
         absorb(j - 1);
 
+        // A piece that is its whole unit gives the outputs at once; others go to the joining step.
+        const bool whole = pc.first == 0 && pc.last == (pc.nv + TILE_T - 1) / TILE_T;
         const size_t slot = (size_t)blockIdx.x + unit;
+        float o[NC];
+        {
+          float v[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          float v0, v1, a0, a1;
-          tc::f2_unpack(l[c / 2], v0, v1);
-          tc::f2_unpack(acc[c / 2], a0, a1);
-          float v = c % 2 ? v1 : v0;
+          for (int c = 0; c < NP; ++c) {
+            tc::f2_unpack(l[c], v[2 * c], v[2 * c + 1]);
+            tc::f2_unpack(acc[c], o[2 * c], o[2 * c + 1]);
+          }
+          int row;
+          const float sum = warp_row_sums<NC>(v, &row);
+          smax[warp * NC + row] = sum;  // (the lanes of one row write the same)
+        }
+        if (!whole && tid < D) {
+          float* to = p.part_o + slot * p.cols * D + tid;
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          if (lane == 0) smax[warp * NC + c] = v;
-          if (c < p.cols && tid < D) p.part_o[(slot * p.cols + c) * D + tid] = c % 2 ? a1 : a0;
+          for (int c = 0; c < NC; ++c)
+            if (c < p.cols) to[c * D] = o[c];
         }
         softmax_sync();
-        if (tid < p.cols)
-          reinterpret_cast<float2*>(p.part_ml)[slot * p.cols + tid] =
-              make_float2(fmax_row[tid], (smax[tid] + smax[NC + tid]) + (smax[2 * NC + tid] + smax[3 * NC + tid]));
+        if (tid < p.cols) {
+          const float m = fmax_row[tid];
+          const float sum = ((smax[tid] + smax[NC + tid]) + smax[2 * NC + tid]) + smax[3 * NC + tid];
+          reinterpret_cast<float2*>(p.part_ml)[slot * p.cols + tid] = make_float2(m, sum);
+          if (whole && p.lse != nullptr)
+            p.lse[(size_t)unit * p.cols + tid] =
+                sum == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(sum)) * 0.6931471805599453f;
+        }
+        if (whole && tid < D) {
+          float sum[NC], u[NC];
+          load_row<NC>(smax, sum);
+#pragma unroll
+          for (int w = 1; w < 4; ++w) {
+            load_row<NC>(smax + w * NC, u);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) sum[c] += u[c];
+          }
+          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.o) + (size_t)unit * p.cols * D + tid;
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            if (c < p.cols)  // sum = 0 exactly when the row sees no token (a NaN score makes it NaN, and the row's o)
+              to[c * D] = __float2bfloat16_rn(sum[c] == 0.f ? 0.f : __fdividef(o[c], sum[c]));
+        }
         if (!more) break;
         const int* f = follow + (piece & 1) * 6;
         pc.b = f[1];
