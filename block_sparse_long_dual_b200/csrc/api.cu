@@ -499,7 +499,7 @@ int cache8_row(const sfa_shape* s) { return (s->seq_len + 127) / 128 * 128; }
 sfa_status cache8_cols(const sfa_shape* s, int nq, int* cols) {
   if (nq < 1) return SFA_ERR_INVALID_ARG;
   const long long c = (long long)nq * (s->heads_q / s->heads_kv);
-  if (c > c8::kMaxCols || (long long)s->batch * s->heads_kv * c >= (1LL << 31)) return SFA_ERR_UNSUPPORTED;
+  if (c > c8::kMaxCols || (long long)s->batch * s->heads_kv >= (1LL << 27)) return SFA_ERR_UNSUPPORTED;
   *cols = (int)c;
   return SFA_OK;
 }

@@ -59,8 +59,12 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // the lengths.  A share that crosses a head's end is cut there; the piece of
 // unit u = b Hkv + g in CTA i has the partial-result slot i + u (both only grow
 // along the list, and one grows at every cut, so no two pieces share a slot).
-// All tiles together are fewer than 2^31 (B Hkv L is), so the list is indexed in
-// 32 bits.
+// A piece costs about as much as two tiles of 128 tokens (start, last O^T,
+// results), so every unit counts for unit_cost more tiles than it has, in front:
+// shares are equal in cost, and a CTA of many short units gets fewer tiles (64
+// sequences x 8 heads of 0 .. 500 tokens: 19.8 us, 24.7 with shares equal in
+// tiles, 20.9 with one tile a piece; long contexts the same).
+// The list is indexed in 32 bits: B Hkv L is under 2^31, B Hkv under 2^27.
 // ---------------------------------------------------------------------------
 constexpr int kSms = 148, kCtasPerSm = 2;
 constexpr int kMaxCols = 16;  // query rows (heads of the group x query tokens) of a unit
@@ -70,16 +74,22 @@ constexpr int kMaxCols = 16;  // query rows (heads of the group x query tokens) 
 __host__ __device__ constexpr int tile_tokens(int D, int cols) { return D == 64 && cols <= 8 ? 256 : 128; }
 
 struct Split {
-  int total;  // tiles of all units
-  int G;      // CTAs with a share: as many as launched, or one per tile where there are fewer tiles,
+  int total;  // cost of all units, in tiles
+  int G;      // CTAs with a share: as many as launched, or one per tile of cost where that is less,
               // so that no share between two others is empty
-  int q, r;   // the first r CTAs take q + 1 tiles, the others q
-  __device__ Split(int t, int launched) : total(t), G(t < launched ? t : launched) {
-    q = G > 0 ? total / G : 0;
-    r = G > 0 ? total % G : 0;
+  int q, r;   // the first r CTAs take q + 1, the others q
+  __device__ Split(int t, int launched) : total(t), G(t < launched ? t : launched), q(1), r(0) {
+    if (t > launched) {
+      q = total / G;
+      r = total - q * G;
+    }
   }
+  __device__ bool one_each() const { return total == G; }
   __device__ int start(int i) const { return i < G ? i * q + min(i, r) : total; }
-  __device__ int owner(int t) const { return t < r * (q + 1) ? t / (q + 1) : r + (t - r * (q + 1)) / q; }
+  __device__ int owner(int t) const {
+    if (one_each()) return t;
+    return t < r * (q + 1) ? t / (q + 1) : r + (t - r * (q + 1)) / q;
+  }
 };
 
 __device__ __forceinline__ int visible(const int* lens, int b, int L, int back, int* status) {
@@ -91,61 +101,96 @@ __device__ __forceinline__ int visible(const int* lens, int b, int L, int back, 
   return n > back ? n - back : 0;
 }
 
-// One warp, all lanes: the tiles of 32 sequences from b0 on, as an inclusive sum per lane.
-__device__ __forceinline__ int warp_scan_tiles(const int* lens, int b0, int B, int Hkv, int L, int back, int tile,
-                                               int* mine, int* status) {
-  const int lane = threadIdx.x & 31, b = b0 + lane;
-  *mine = b < B ? (visible(lens, b, L, back, status) + tile - 1) / tile * Hkv : 0;
-  int inc = *mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += u;
-  }
-  return inc;
+// Tiles of a head of sequence b (0: none visible).
+__device__ __forceinline__ int head_tiles(const int* lens, int b, int B, int L, int back, int tile, int* status) {
+  return b < B ? (visible(lens, b, L, back, status) + tile - 1) / tile : 0;
 }
 
-// One warp: tiles of the whole batch, and of the sequences before b_at.
-__device__ __forceinline__ int warp_count_tiles(const int* lens, int B, int Hkv, int L, int back, int tile, int b_at,
-                                                int* before) {
-  int all = 0, pre = 0;
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    int mine;
-    const int inc = warp_scan_tiles(lens, b0, B, Hkv, L, back, tile, &mine, nullptr);
-    if (b_at >= b0 && b_at < b0 + 32) pre = all + __shfl_sync(0xffffffffu, inc - mine, b_at - b0);
-    all += __shfl_sync(0xffffffffu, inc, 31);
+__device__ __forceinline__ int warp_inclusive(int x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += u;
   }
-  *before = pre;
-  return all;
+  return x;
+}
+
+// What a unit costs beside its tiles: nothing where every tile has a CTA to itself.
+__device__ __forceinline__ int unit_cost(int tiles, int launched, int tile) {
+  return tiles <= launched ? 0 : tile == 128 ? 2 : 1;
+}
+
+// One warp: cost of the whole batch (*total), the cost that each unit of it has beside its tiles, and (returned) the
+// cost of the sequences before b_at.
+__device__ __forceinline__ int warp_count_cost(const int* lens, int B, int Hkv, int L, int back, int tile, int launched,
+                                               int b_at, int* total, int* per_unit) {
+  const int lane = threadIdx.x & 31;
+  int all = 0, seqs = 0, pre = 0, pre_seqs = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int t = head_tiles(lens, b0 + lane, B, L, back, tile, nullptr);
+    const unsigned some = __ballot_sync(0xffffffffu, t > 0);
+    const bool in_front = b0 + lane < b_at;
+    pre += (int)__reduce_add_sync(0xffffffffu, (unsigned)(in_front ? t : 0));
+    all += (int)__reduce_add_sync(0xffffffffu, (unsigned)t);
+    pre_seqs += __popc(some & __ballot_sync(0xffffffffu, in_front));
+    seqs += __popc(some);
+  }
+  *per_unit = unit_cost(all * Hkv, launched, tile);
+  *total = (all + *per_unit * seqs) * Hkv;
+  return (pre + *per_unit * pre_seqs) * Hkv;
 }
 
 // One warp: the share of CTA i of `launched`: its tiles (0: none), its first sequence, and that sequence's tiles
 // before the share.
 __device__ __forceinline__ int warp_share(const int* lens, int B, int Hkv, int L, int back, int tile, int launched,
                                           int i, int* b_first, int* skip, int* status) {
-  int mine, inc = warp_scan_tiles(lens, 0, B, Hkv, L, back, tile, &mine, status);
-  int total = __shfl_sync(0xffffffffu, inc, 31);
+  const int lane = threadIdx.x & 31;
+  const unsigned upto = 0xffffffffu >> (31 - lane);
+  const int t0 = head_tiles(lens, lane, B, L, back, tile, status);
+  const int tin0 = warp_inclusive(t0);
+  int all = __shfl_sync(0xffffffffu, tin0, 31), seqs = __popc(__ballot_sync(0xffffffffu, t0 > 0));
   for (int b0 = 32; b0 < B; b0 += 32) {
-    int m2;
-    total += __shfl_sync(0xffffffffu, warp_scan_tiles(lens, b0, B, Hkv, L, back, tile, &m2, status), 31);
+    const int t = head_tiles(lens, b0 + lane, B, L, back, tile, status);
+    all += (int)__reduce_add_sync(0xffffffffu, (unsigned)t);
+    seqs += __popc(__ballot_sync(0xffffffffu, t > 0));
   }
-  const Split s(total, launched);
-  const int x0 = s.start(i), n = s.start(i + 1) - x0;
+  const int extra = unit_cost(all * Hkv, launched, tile);
+  const Split s((all + extra * seqs) * Hkv, launched);
+  const int x1 = s.start(i + 1);
+  int x = s.start(i);
   *b_first = *skip = 0;
-  if (n <= 0) return 0;
-  int base = 0;
+  if (x1 <= x) return 0;
+  // Tiles of the list before the costs x0 and x1.
+  int cost_in_front = 0, tiles_in_front = 0, from = -1;
   for (int b0 = 0; b0 < B; b0 += 32) {
-    if (b0 > 0) inc = warp_scan_tiles(lens, b0, B, Hkv, L, back, tile, &mine, nullptr);
-    const unsigned in = __ballot_sync(0xffffffffu, x0 < base + inc);
-    if (in != 0) {
+    const int t = b0 == 0 ? t0 : head_tiles(lens, b0 + lane, B, L, back, tile, nullptr);
+    const int tin = b0 == 0 ? tin0 : warp_inclusive(t);
+    const unsigned some = __ballot_sync(0xffffffffu, t > 0);
+    const int inc = cost_in_front + (tin + extra * __popc(some & upto)) * Hkv;
+#pragma unroll 1
+    for (;;) {
+      const unsigned in = __ballot_sync(0xffffffffu, x < inc);
+      if (in == 0) break;
       const int l = __ffs(in) - 1;
+      const int tl = __shfl_sync(0xffffffffu, t, l), cost = tl + extra;
+      const int y = x - __shfl_sync(0xffffffffu, inc, l) + cost * Hkv;  // cost into the sequence
+      int g = (int)__fdividef((float)y, (float)cost);                  // off by one at most for Hkv < 2^20
+      while (g * cost > y) --g;
+      while (y - g * cost >= cost) ++g;
+      const int here = g * tl + max(y - g * cost - extra, 0);
+      const int at = tiles_in_front + __shfl_sync(0xffffffffu, tin - t, l) * Hkv + here;
+      if (from >= 0) return at - from;
+      from = at;
       *b_first = b0 + l;
-      *skip = x0 - base - __shfl_sync(0xffffffffu, inc - mine, l);
-      return n;
+      *skip = here;
+      if (s.one_each()) return 1;
+      x = x1;
     }
-    base += __shfl_sync(0xffffffffu, inc, 31);
+    cost_in_front = __shfl_sync(0xffffffffu, inc, 31);
+    tiles_in_front += __shfl_sync(0xffffffffu, tin, 31) * Hkv;
   }
-  return 0;  // only if the lengths changed under the call
+  return from < 0 ? 0 : tiles_in_front - from;  // to the end; 0 only if the lengths changed under the call
 }
 
 }  // namespace c8

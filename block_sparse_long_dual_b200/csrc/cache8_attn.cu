@@ -50,9 +50,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attn_join_kernel(const __grid
   const int part0 = join ? 0 : (int)((blockIdx.x - rows) % parts) * per_part;  // this CTA's tokens
   if (!join && part0 >= nv) return;
   if (tid < 32) {
-    int before;
-    const int total = warp_count_tiles(p.lens, p.B, p.Hkv, p.L, p.back, p.tile, b, &before);
-    if (tid == 0) { sh_total = total; sh_t0 = before + g * tiles; }
+    int total, extra;
+    const int before = warp_count_cost(p.lens, p.B, p.Hkv, p.L, p.back, p.tile, p.G, b, &total, &extra);
+    if (tid == 0) { sh_total = total; sh_t0 = before + g * (tiles + extra) + extra; }
   }
   __syncthreads();
   size_t s0 = 0;  // the unit's pieces have the slots [s0, s0 + np)

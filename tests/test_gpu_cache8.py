@@ -209,6 +209,11 @@ ATTNS = [  # B, Hkv, G, cap, d, block, nq, back, lens, spread
     (4, 2, 2, 50, 64, 64, 1, 0, (0, 0, 0, 0), 0),     # nothing anywhere
     (3, 2, 1, 600, 64, 64, 8, 0, (259, 512, 258), 2),  # the causal edge over two tiles of 256
     (3, 1, 1, 300, 128, 128, 8, 0, (130, 256, 263), 1),  # and of 128
+    # more tiles than CTAs: shares that cross units
+    (64, 8, 4, 500, 128, 64, 1, 0, tuple(i * 37 % 501 for i in range(64)), 1),
+    (70, 8, 1, 700, 64, 64, 2, 0, tuple(i * 211 % 701 if i % 5 else 0 for i in range(70)), 1),
+    (3, 8, 2, 2600, 128, 128, 4, 5, (2600, 1300, 2599), 1),
+    (1, 1, 1, 38100, 128, 128, 1, 0, (38100,), 0),
 ]
 
 
