@@ -146,21 +146,21 @@ __global__ void advance_kernel(Cache8Append p) {
 // evict, selection: a cluster of CS CTAs per (b, KV head), each over a contiguous
 // slice of the tokens.  Radix select (11 + 11 + 10 bits) of the order-preserving
 // weight keys.  The slices' histograms are summed through distributed shared
-// memory, each CTA an eighth of the bins; every CTA then finds the eighth and the
-// bin of the threshold.  A slice's own histogram also tells how many kept rows lie
-// before the next slice's.  The slice's keys stay in shared memory through all
-// passes (a longer slice is read again in each pass) and the loops over them are
-// short code: keys in registers meant every loop unrolled, run once or three
-// times, and waiting for instructions.  Accumulated weights share few leading
-// bits, so neighbouring lanes would queue on one bin: two copies of the histogram,
-// sixteen banks apart.
+// memory, each CTA an eighth of the bins (all bins in every CTA: 59 against 54.8
+// us); every CTA then finds the eighth and the bin of the threshold.  A slice's
+// own histogram also tells how many kept rows lie before the next slice's.  The
+// slice stays in shared memory through all passes (a longer one is read again in
+// each pass): copied there asynchronously, all of it on its way at once, the
+// first pass puts the keys in place.  The loops are short code: unrolled code
+// that runs once waits for its instructions (keys in registers: 7 us more).
+// One histogram serves: with two or four copies, lanes apart, 53.5 and 55.5 us
+// against 53.3, with equal weights everywhere 57.5 against 57.2.
+// 131072 -> 8192 tokens of 4 x 8 heads: the selection takes 26 us for 17 MB (hist
+// and meetings 6 us each, the copy 4), and is bound by these steps' latencies.
 // ---------------------------------------------------------------------------
 constexpr int kSlice = 16384;  // keys in shared memory
-constexpr int kBins = 2048, kBinStride = kBins + 16;
-// One word of padding per 32 keys: neighbouring keys and keys a small power of two apart spread over the banks.
-__device__ __forceinline__ int key_at(int i) { return i + (i >> 5); }
-constexpr int kKeyWords = kSlice + kSlice / 32;
-constexpr size_t kSelSmem = ((size_t)kKeyWords + 2 * kBinStride) * sizeof(uint32_t);
+constexpr int kBins = 2048;
+constexpr size_t kSelSmem = ((size_t)kSlice + kBins) * sizeof(uint32_t);
 
 // Exclusive sum over the block of a 32-bit value.
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* wsum) {
@@ -181,10 +181,10 @@ template <int CS, int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __grid_constant__ Cache8Evict p) {
   constexpr int kBpt = kBins / kSelThreads;  // bins per thread
   extern __shared__ __align__(16) uint32_t sel_smem[];
-  uint32_t* key = sel_smem;                // [kKeyWords], through key_at
-  uint32_t* hist = sel_smem + kKeyWords;   // [2][kBinStride]
-  __shared__ __align__(16) uint32_t fold[2][CS > 1 ? kBins : 2];  // this slice's bins (two: a pass may begin while others read)
-  __shared__ uint32_t part[2][CS > 1 ? kBins / CS : 1], ptotal[2];  // this CTA's share of the bins, over all slices
+  uint32_t* key = sel_smem;             // [kSlice]
+  uint32_t* hist = sel_smem + kSlice;   // [kBins]
+  __shared__ uint32_t part[CS > 1 ? kBins / CS : 1];  // this CTA's share of the bins, over all slices
+  __shared__ uint32_t ptotal[2];  // and their sum (two: the next pass begins while others read)
   __shared__ uint32_t wsum[kSelThreads / 32];
   __shared__ uint32_t share[2];  // this slice's keys above and at the threshold
   __shared__ uint32_t sh_digit, sh_above;
@@ -215,13 +215,15 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
     __syncthreads();  // everyone is done with the keys before
     first = from;
     cnt = min(kSlice, hi - from);
-#pragma unroll 8
-    for (int i = tid; i < cnt; i += kSelThreads) key[key_at(i)] = weight_key(__ldg(w + from + i));
+#pragma unroll 4
+    for (int i = tid; i < cnt; i += kSelThreads)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(key + i)), "l"(w + from + i) : "memory");
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
   };
   const bool whole = hi - lo <= kSlice;
   if (tid < 2) share[tid] = 0;
-  for (int i = tid; i < 2 * kBinStride; i += kSelThreads) hist[i] = 0;
+  for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
   if (whole) load(lo);
   else __syncthreads();
 
@@ -230,13 +232,21 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), up = pass == 1 ? 21 : 10;
     const uint32_t mask = pass == 2 ? 1023u : 2047u;  // (the last pass leaves the upper bins empty)
-    uint32_t* copy = hist + (lane & 1) * kBinStride;
     for (int from = lo; from < hi; from += kSlice) {
       if (!whole) load(from);
-#pragma unroll 4
-      for (int i = tid; i < cnt; i += kSelThreads) {
-        const uint32_t k = key[key_at(i)];
-        if (pass == 0 || (k >> up) == prefix) atomicAdd(copy + ((k >> shift) & mask), 1u);
+#pragma unroll 2
+      for (int i = 4 * tid; i < cnt; i += 4 * kSelThreads) {
+        uint4* at = reinterpret_cast<uint4*>(key + i);
+        uint4 x = *at;
+        if (pass == 0 || !whole) {
+          x = make_uint4(weight_key(__uint_as_float(x.x)), weight_key(__uint_as_float(x.y)),
+                         weight_key(__uint_as_float(x.z)), weight_key(__uint_as_float(x.w)));
+          if (whole) *at = x;
+        }
+        const uint32_t k[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i + j < cnt && (pass == 0 || (k[j] >> up) == prefix)) atomicAdd(hist + ((k[j] >> shift) & mask), 1u);
       }
     }
     __syncthreads();
@@ -246,25 +256,19 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
     uint32_t own[kBpt];
 #pragma unroll
     for (int j = 0; j < kBpt; j += 2) {
-      uint2* h = reinterpret_cast<uint2*>(hist + bin0 + j);
-      uint2* g = reinterpret_cast<uint2*>(hist + kBinStride + bin0 + j);
-      const uint2 u = *h, v = *g;
-      own[j] = u.x + v.x;
-      own[j + 1] = u.y + v.y;
-      *h = *g = make_uint2(0, 0);
+      const uint2 u = *reinterpret_cast<const uint2*>(hist + bin0 + j);
+      own[j] = u.x;
+      own[j + 1] = u.y;
     }
     if (CS > 1) {
       constexpr int PB = kBins / CS;
-      uint32_t *mine = fold[pass & 1], *sum = part[pass & 1];
-#pragma unroll
-      for (int j = 0; j < kBpt; j += 2) *reinterpret_cast<uint2*>(mine + bin0 + j) = make_uint2(own[j], own[j + 1]);
       if (tid == 0) ptotal[pass & 1] = 0;
       cluster.sync();
       if (tid < PB) {
         uint32_t v = 0;
 #pragma unroll
-        for (int q = 0; q < CS; ++q) v += cluster.map_shared_rank(mine, q)[rank * PB + tid];
-        sum[tid] = v;
+        for (int q = 0; q < CS; ++q) v += cluster.map_shared_rank(hist, q)[rank * PB + tid];
+        part[tid] = v;
         v = __reduce_add_sync(0xffffffffu, v);
         if (lane == 0 && v != 0) atomicAdd(&ptotal[pass & 1], v);
       }
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
         }
         run += v;
       }
-      const uint32_t v = tid < PB ? cluster.map_shared_rank(sum, e)[PB - 1 - tid] : 0u;
+      const uint32_t v = tid < PB ? cluster.map_shared_rank(part, e)[PB - 1 - tid] : 0u;
       const uint32_t before = skipped + block_scan(v, wsum);
       if (tid < PB && before < need && before + v >= need) {
         sh_digit = (uint32_t)(e * PB + PB - 1 - tid);
@@ -302,6 +306,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
         before += own[j];
       }
     }
+#pragma unroll
+    for (int j = 0; j < kBpt; j += 2) *reinterpret_cast<uint2*>(hist + bin0 + j) = make_uint2(0, 0);
     __syncthreads();
     const uint32_t digit = sh_digit;
     uint32_t above = 0;
@@ -329,25 +335,40 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
   }
   for (int from = lo; from < hi; from += kSlice) {
     if (!whole) load(from);
-    const int span = (cnt + kSelThreads - 1) / kSelThreads;  // this thread: the keys [k0, k1)
-    const int k0 = min(tid * span, cnt), k1 = min(k0 + span, cnt);
-    uint32_t pk = 0;  // (greater << 16) | equal: 16384 keys at most
+    // Rows of 32 keys, a warp's one after the other, each lane with the votes of one of them.
+    const int rows = (cnt + 31) / 32, per_warp = (rows + kSelThreads / 32 - 1) / (kSelThreads / 32);
+    const int row0 = (tid >> 5) * per_warp;
+    uint32_t vg = 0, ve = 0;
 #pragma unroll 4
-    for (int i = k0; i < k1; ++i) {
-      const uint32_t k = key[key_at(i)];
-      pk += k > prefix ? 65536u : (k == prefix ? 1u : 0u);
+    for (int r = 0; r < per_warp; ++r) {
+      const int i = (row0 + r) * 32 + lane;
+      uint32_t k = i < cnt ? key[i] : 0u;
+      if (!whole) k = weight_key(__uint_as_float(k));
+      const uint32_t g = __ballot_sync(0xffffffffu, i < cnt && k > prefix);
+      const uint32_t e = __ballot_sync(0xffffffffu, i < cnt && k == prefix);
+      if (lane == r) { vg = g; ve = e; }
     }
-    const uint32_t before = block_scan(pk, wsum);
+    const uint32_t before = block_scan(((uint32_t)__popc(vg) << 16) | (uint32_t)__popc(ve), wsum);  // 16384 keys at most
     uint32_t g = gt + (before >> 16), e = eq + (before & 0xFFFFu);
-    if (pk != 0) {
-#pragma unroll 4
-      for (int i = k0; i < k1; ++i) {
-        const uint32_t k = key[key_at(i)];
-        if (k >= prefix) {
-          if (k > prefix || e < need) out[g + min(e, need)] = first + i;
-          g += k > prefix;
-          e += k == prefix;
-        }
+    uint32_t v = vg | ve;
+    if ((int)__reduce_max_sync(0xffffffffu, (unsigned)__popc(v)) <= per_warp) {  // a lane a row
+      const int row = first + (row0 + lane) * 32;
+      for (; v != 0; v &= v - 1) {
+        const int at = __ffs(v) - 1;
+        const bool more = (vg >> at) & 1u;
+        if (more || e < need) out[g + min(e, need)] = row + at;
+        g += more;
+        e += !more;
+      }
+    } else {  // a lane a key
+      const uint32_t under = (1u << lane) - 1u;
+#pragma unroll 1
+      for (int r = 0; r < per_warp; ++r) {
+        const uint32_t rg = __shfl_sync(0xffffffffu, vg, r), re = __shfl_sync(0xffffffffu, ve, r);
+        const uint32_t kg = __shfl_sync(0xffffffffu, g, r) + __popc(rg & under);
+        const uint32_t ke = __shfl_sync(0xffffffffu, e, r) + __popc(re & under);
+        const bool more = (rg >> lane) & 1u;
+        if (more || (((re >> lane) & 1u) && ke < need)) out[kg + min(ke, need)] = first + (row0 + r) * 32 + lane;
       }
     }
     if (!whole) {  // wsum still holds the warps' totals
