@@ -599,11 +599,13 @@ sfa_status sfa_cache8_attn(const sfa_shape* shape, const sfa_cache8* cache, cons
   p.part_ml = reinterpret_cast<float*>(ws + w.ml);
   p.part_o = reinterpret_cast<float*>(ws + w.o);
   p.scores = weight_out != nullptr ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
-  p.nq = nq; p.cols = cols; p.cpad = cache8_cpad(cols); p.back = back; p.tile = c8::tile_tokens(p.D, cols); p.G = cache8_ctas(shape, cols); p.Lp = cache8_row(shape);
+  p.nq = nq; p.cols = cols; p.cpad = cache8_cpad(cols); p.back = back;
+  p.tile = c8::tile_tokens(p.D, cols); p.G = cache8_ctas(shape, cols); p.Lp = cache8_row(shape);
   p.sl2 = (scale > 0.f ? scale : (float)(1.0 / sqrt((double)shape->head_dim))) * 1.4426950408889634f;
   CUtensorMap tk, tv;
   const uint64_t rows = (uint64_t)p.B * p.Hkv * p.L;
-  if (!make_code_map(&tk, cache->k, rows, p.D, p.tile) || !make_code_map(&tv, cache->v, rows, p.D, p.tile)) return SFA_ERR_CUDA;
+  if (!make_code_map(&tk, cache->k, rows, p.D, p.tile) || !make_code_map(&tv, cache->v, rows, p.D, p.tile))
+    return SFA_ERR_CUDA;
   return cuda_status(launch_cache8_attn(p, tk, tv, as_stream(stream)));
 }
 
@@ -655,6 +657,10 @@ sfa_status sfa_cache8_evict(const sfa_shape* shape, const sfa_cache8* src, const
         (reinterpret_cast<uintptr_t>(workspace) & 255))
       return SFA_ERR_WORKSPACE;
     idx = static_cast<int*>(workspace);
+  }
+  for (int i = 0; i < 6; ++i) {  // the rows are moved by this list
+    const size_t bytes = units * keep * sizeof(int);
+    if (overlap(idx, bytes, a[i], na[i]) || overlap(idx, bytes, d[i], nd[i])) return SFA_ERR_INVALID_ARG;
   }
   Cache8Evict p;
   p.k = static_cast<const uint8_t*>(src->k); p.v = static_cast<const uint8_t*>(src->v);

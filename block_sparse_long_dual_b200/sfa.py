@@ -793,7 +793,7 @@ class KvCache8:
         graph is captured: the call then takes one from that graph's pool, so that no two graphs share it."""
         if torch.cuda.is_current_stream_capturing():
             return None
-        key = (q.shape[1], q.shape[2] if q.dim() == 4 else 1, weights, _handle(self._launch(stream)[1]))
+        key = (q.shape[1:-1], weights, _handle(self._launch(stream)[1]))
         if key not in self._workspaces:
             self._workspaces[key] = _fresh(torch.empty(cache8_attn_workspace(q, self, weights=weights),
                                                        dtype=torch.uint8, device=self.k.device), stream)

@@ -455,8 +455,8 @@ size_t sfa_cache8_evict_workspace(const sfa_shape* shape, int keep);
  * required), dst lens[b] = min(n, keep).  dst rows, scales and weights behind
  * the kept ones are left as they were.  idx [B, heads_kv, keep] int32
  * (nullable): the kept tokens' src rows ascending, padded with -1.
- * 1 <= keep, 0 <= recent <= keep.  dst's arrays must not overlap src's
- * (SFA_ERR_INVALID_ARG).  A bad length counts as 0 and sets status_word.
+ * 1 <= keep, 0 <= recent <= keep.  dst's arrays must not overlap src's,
+ * nor idx (or the workspace) either's (SFA_ERR_INVALID_ARG).  A bad length counts as 0 and sets status_word.
  * workspace (256-byte aligned) is used only where idx is NULL.
  */
 sfa_status sfa_cache8_evict(const sfa_shape* shape, const sfa_cache8* src, const sfa_cache8* dst,

@@ -106,7 +106,9 @@ def test_evict(lib):
     assert evict(lib, b=dst(block=64)) == 2
     assert evict(lib, b=dst(k=(1 << 30) + 64)) == 1      # into the source's keys
     assert evict(lib, b=dst(lens=(3 << 30) + (2 << 20))) == 1
+    assert evict(lib, idx=(1 << 30) + 1024) == 1 and evict(lib, idx=(7 << 30) - 16) == 1  # the list in a cache
     need = lib.sfa_cache8_evict_workspace(ctypes.byref(S()), 100)
+    assert evict(lib, idx=None, ws=6 << 30, n=need) == 1
     assert need >= 2 * 2 * 100 * 4
     assert evict(lib, idx=None) == 5 and evict(lib, idx=None, ws=P, n=need - 1) == 5
     assert lib.sfa_cache8_evict_workspace(ctypes.byref(S()), 0) == 0
