@@ -20,8 +20,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 // a row; the others, with weights, each add the attention weights of some chunks of tokens
 // of one unit: the rows' log-sum-exps again from the pieces' maxima and sums (a few
 // numbers), then exp2 of the scores that the first step left, summed over the
-// rows in order.  Launched while the first step still runs: everything up to
-// pieces_ready() needs only the lengths.
+// rows in order.  A unit of one piece has its outputs from the first step already.
+// Launched while the first step still runs: everything up to pieces_ready() needs
+// only the lengths.  At 16 x 8 units of 4 rows over 32768 tokens it adds 4 us to the
+// 160 of the first step; with weights, 4 x 8 units over 131072 tokens, 21 us for
+// 67 MB of scores, 17 of weights read and 17 written: 4.8 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
@@ -233,6 +236,9 @@ static cudaError_t launch_join_d(const Cache8Attn& p, cudaStream_t st) {
 // tokens, BATCH of them with both loads in flight, and the groups are
 // joined at the end.  The list is checked and staged in shared memory first
 // (kListPart entries at a time), so that a row's address waits for no second load.
+// 512 rows of 1023 of up to 16383 tokens, d 128: 33.3 us for 139 MB of rows, 4.2 TB/s:
+// bound by rows of 128 bytes at random addresses and by the instructions that
+// widen the codes (issue 63%).
 // ---------------------------------------------------------------------------
 constexpr int kListPart = 2048;
 
