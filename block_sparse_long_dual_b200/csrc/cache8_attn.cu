@@ -1,5 +1,6 @@
 // Attention over the 8-bit KV cache: joining the pieces of the whole-cache attention
 // (cache8_attn_tc.cu), the accumulated weights, and index lists.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include "cache8.cuh"
@@ -10,6 +11,7 @@ namespace sfa {
 namespace {
 
 using namespace c8;
+namespace cg = cooperative_groups;
 
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -231,25 +233,31 @@ static cudaError_t launch_join_d(const Cache8Attn& p, cudaStream_t st) {
 }
 
 // ---------------------------------------------------------------------------
-// Index lists: CTA per (b, q head).  A row of d codes is read by d / 16 lanes,
+// Index lists: a CTA, or two that join their halves, per (b, q head).  A row of d codes is read by d / 16 lanes,
 // 16 bytes each; each such lane group runs its own online softmax over its
 // tokens, BATCH of them with both loads in flight, and the groups are
 // joined at the end.  The list is checked and staged in shared memory first
 // (kListPart entries at a time), so that a row's address waits for no second load.
-// 512 rows of 1023 of up to 16383 tokens, d 128: 33.3 us for 139 MB of rows, 4.2 TB/s:
-// bound by rows of 128 bytes at random addresses and by the instructions that
-// widen the codes (issue 63%).
+// 512 rows of 1023 of up to 16383 tokens, d 128: 31.7 us for 139 MB of rows, 4.4 TB/s:
+// bound by rows of 128 bytes at random addresses, the chain from a row to its
+// probability, and the instructions that widen the codes (issue 63%).  Rows through a
+// ring of asynchronous copies: 37.4 us; o rescaled only where the maximum grows: 32.6.
 // ---------------------------------------------------------------------------
 constexpr int kListPart = 2048;
 
-template <int D, int WARPS, int BATCH, int CTAS>
+template <int D, int WARPS, int BATCH, int CTAS, int CL>
 __global__ void __launch_bounds__(WARPS * 32, CTAS) attn_list_kernel(const __grid_constant__ Cache8Attn p) {
   constexpr int LPT = D / 16, GROUPS = WARPS * 32 / LPT;
   __shared__ int list[kListPart];
   __shared__ float gm[GROUPS], gl[GROUPS];
   __shared__ __align__(16) float go[GROUPS][D + 4];
   __shared__ int bad;
-  const int row = blockIdx.x, b = row / p.Hq, h = row % p.Hq, g = h / (p.Hq / p.Hkv);
+  __shared__ float other[D + 2];  // CL = 2: the second CTA's o, maximum and sum
+  __shared__ int other_bad;
+  cg::cluster_group cluster = cg::this_cluster();
+  if (CL > 1) cluster.barrier_arrive();  // waited for before the first access to the other CTA
+  const int rank = CL > 1 ? (int)cluster.block_rank() : 0;
+  const int row = blockIdx.x / CL, b = row / p.Hq, h = row % p.Hq, g = h / (p.Hq / p.Hkv);
   const int unit = b * p.Hkv + g;
   const int tid = threadIdx.x, grp = tid / LPT, part = tid % LPT;
   const int* src = p.idx + (size_t)row * p.k_list;
@@ -277,8 +285,9 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) attn_list_kernel(const __gri
   float m = -INFINITY, l = 0.f, acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-  for (int from = 0; from < p.k_list; from += kListPart) {
-    const int have = min(kListPart, p.k_list - from);
+  const int half = (p.k_list + CL - 1) / CL, end = min(rank * half + half, p.k_list);
+  for (int from = rank * half; from < end; from += kListPart) {
+    const int have = min(kListPart, end - from);
     __syncthreads();
     for (int i = tid; i < have; i += WARPS * 32) {
       int t = __ldg(src + from + i);
@@ -345,8 +354,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) attn_list_kernel(const __gri
     *reinterpret_cast<float4*>(&go[grp][part * 16 + e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
   __syncthreads();
   if (bad && tid == 0) report(p.status, SFA_ERR_INDEX);
+  float M = -INFINITY, L = 0.f, o = 0.f;
   if (tid < D) {
-    float M = -INFINITY, L = 0.f, o = 0.f;
 #pragma unroll 8
     for (int i = 0; i < GROUPS; ++i) M = fmaxf(M, gm[i]);
     const float base = M == -INFINITY ? 0.f : M;
@@ -356,10 +365,56 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) attn_list_kernel(const __gri
       L += gl[i] * f;
       o = fmaf(go[i][tid], f, o);
     }
-    const bool none = bad || L == 0.f;
-    static_cast<__nv_bfloat16*>(p.o)[(size_t)row * D + tid] = __float2bfloat16_rn(none ? 0.f : o / L);
-    if (tid == 0 && p.lse != nullptr) p.lse[row] = none ? -INFINITY : (base + log2f(L)) * kLn2;
   }
+  bool broken = bad;
+  if (CL > 1) {
+    cluster.barrier_wait();
+    if (rank == 1) {
+      float* to = cluster.map_shared_rank(other, 0);
+      if (tid < D) to[tid] = o;
+      if (tid == 0) {
+        to[D] = M;
+        to[D + 1] = L;
+        *cluster.map_shared_rank(&other_bad, 0) = bad;
+      }
+    }
+    cluster.sync();
+    if (rank == 1) return;
+    broken |= other_bad != 0;
+    const float m1 = other[D], mn = fmaxf(M, m1), base = mn == -INFINITY ? 0.f : mn;
+    const float f0 = exp2f(M - base), f1 = exp2f(m1 - base);
+    L = L * f0 + other[D + 1] * f1;
+    if (tid < D) o = o * f0 + other[tid] * f1;
+    M = mn;
+  }
+  if (tid < D) {
+    const bool none = broken || L == 0.f;
+    static_cast<__nv_bfloat16*>(p.o)[(size_t)row * D + tid] = __float2bfloat16_rn(none ? 0.f : o / L);
+    if (tid == 0 && p.lse != nullptr) p.lse[row] = none ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2;
+  }
+}
+
+template <int D>
+cudaError_t launch_list(const Cache8Attn& p, cudaStream_t st) {
+  const unsigned rows = (unsigned)(p.B * p.Hq);
+  // Up to two rows an SM: four tokens in flight a lane group (128 x 256 tokens: 5.4 us, 6.1 with two); more rows:
+  // two tokens and twice the warps an SM (512 x 1023 tokens: 33.5 us, 37.8 with four), in CTAs of half a row, whose
+  // number an SM comes out evener (31.7 us).
+  if (rows <= 2u * kSms) {
+    attn_list_kernel<D, 8, 4, 2, 1><<<rows, 256, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(rows * 2);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_list_kernel<D, 4, 2, 8, 2>, p);
 }
 
 }  // namespace
@@ -370,19 +425,8 @@ cudaError_t launch_cache8_attn(const Cache8Attn& p, const CUtensorMap& tk, const
   return p.D == 128 ? launch_join_d<128>(p, st) : launch_join_d<64>(p, st);
 }
 
-template <int D>
-static void launch_list(const Cache8Attn& p, cudaStream_t st) {
-  const unsigned rows = (unsigned)(p.B * p.Hq);
-  // Up to two rows an SM: four tokens in flight a lane group (128 x 256 tokens: 5.5 us, 6.1 with two); more rows:
-  // two tokens and twice the CTAs a SM (512 x 1023 tokens: 33.5 us, 37.8 with four).
-  if (rows <= 2u * kSms) attn_list_kernel<D, 8, 4, 2><<<rows, 256, 0, st>>>(p);
-  else attn_list_kernel<D, 8, 2, 4><<<rows, 256, 0, st>>>(p);
-}
-
 cudaError_t launch_cache8_attn_list(const Cache8Attn& p, cudaStream_t st) {
-  if (p.D == 128) launch_list<128>(p, st);
-  else launch_list<64>(p, st);
-  return cudaGetLastError();
+  return p.D == 128 ? launch_list<128>(p, st) : launch_list<64>(p, st);
 }
 
 }  // namespace sfa

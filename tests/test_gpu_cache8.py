@@ -432,6 +432,10 @@ LISTS = [  # B, Hkv, G, cap, d, block, k, lens
     (2, 2, 2, 900, 128, 64, 1023, (900, 899)),
     (40, 8, 1, 130, 128, 128, 33, tuple(range(1, 41))),
     (1, 1, 2, 5000, 64, 128, 4500, (5000,)),   # a list staged in parts
+    # more rows than CTAs of whole rows are resident: two CTAs a row
+    (75, 2, 2, 300, 64, 64, 1, tuple(i * 7 % 300 for i in range(75))),
+    (38, 8, 1, 703, 128, 64, 601, tuple(i * 19 for i in range(38))),
+    (38, 1, 8, 900, 64, 128, 4500, (900,) * 38),
 ]
 
 
@@ -469,6 +473,26 @@ def test_list_attention_reports_bad_entries():
     assert int(cache.status.item()) == 8
     assert torch.all(o[0, 1:3] == 0) and torch.isneginf(lse[0, 1:3]).all()
     assert torch.equal(o[0, [0, 3]], good[0, [0, 3]])
+
+
+def test_list_attention_reports_bad_entries_of_either_half():
+    """More rows than fit as whole rows: a list's halves are read by two CTAs, and one bad entry empties the row."""
+    rng = np.random.default_rng(22)
+    arr = Arrays(rng, 50, 2, 200, 128, 128, (100,) * 50)
+    cache = arr.gpu()
+    q = bf16(rng.normal(size=(50, 8, 128))).to(dev())
+    idx = torch.randint(0, 100, (50, 8, 51), dtype=torch.int32, device=dev())
+    good = cache.attend_list(q, idx)
+    assert int(cache.status.item()) == 0
+    idx[3, 1, 0], idx[20, 7, 50], idx[49, 0, 26] = 100, -2, 150
+    lse = torch.empty((50, 8), device=dev())
+    o = cache.attend_list(q, idx, lse=lse)
+    assert int(cache.status.item()) == 8
+    fine = torch.ones((50, 8), dtype=torch.bool, device=dev())
+    for at in ((3, 1), (20, 7), (49, 0)):
+        assert torch.all(o[at] == 0) and torch.isneginf(lse[at])
+        fine[at] = False
+    assert torch.equal(o[fine], good[fine]) and torch.isfinite(lse[fine]).all()
 
 
 # ---------------------------------------------------------------------------
