@@ -151,13 +151,15 @@ __global__ void advance_kernel(Cache8Append p) {
 // us); every CTA then finds the eighth and the bin of the threshold.  A slice's
 // own histogram also tells how many kept rows lie before the next slice's.  The
 // slice stays in shared memory through all passes (a longer one is read again in
-// each pass): copied there asynchronously, all of it on its way at once, the
+// each pass): copied there asynchronously, all of it on its way at once, 16 bytes a
+// copy where the slice starts on 16 bytes (51.4 us, 52.7 with 4 bytes each); the
 // first pass puts the keys in place.  The loops are short code: unrolled code
 // that runs once waits for its instructions (keys in registers: 7 us more).
 // One histogram serves: with two or four copies, lanes apart, 53.5 and 55.5 us
 // against 53.3, with equal weights everywhere 57.5 against 57.2.
-// 131072 -> 8192 tokens of 4 x 8 heads: the selection takes 26 us for 17 MB (hist
-// and meetings 6 us each, the copy 4), and is bound by these steps' latencies.
+// 131072 -> 8192 tokens of 4 x 8 heads (the times above are this whole eviction's):
+// the selection takes 25 us for 17 MB, bound by the latencies of its steps
+// (histograms 6 us, meetings and sums 9, the copy 3, the list 2).
 // ---------------------------------------------------------------------------
 constexpr int kSlice = 16384;  // keys in shared memory
 constexpr int kBins = 2048;
@@ -209,15 +211,20 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const __gr
   for (int i = rank * kSelThreads + tid; i < p.recent; i += CS * kSelThreads) out[want + i] = old + i;
   if (want == 0) return;
 
-  const int per = (old + CS - 1) / CS, lo = min(rank * per, old), hi = min(lo + per, old);
+  const int per = ((old + CS - 1) / CS + 3) & ~3, lo = min(rank * per, old), hi = min(lo + per, old);
   const float* w = p.weight + (size_t)unit * p.L;
   int first = lo, cnt = 0;  // the keys in shared memory: rows [first, first + cnt)
   auto load = [&](int from) {
     __syncthreads();  // everyone is done with the keys before
     first = from;
     cnt = min(kSlice, hi - from);
+    const int quads = (reinterpret_cast<uintptr_t>(w + from) & 15) == 0 ? cnt / 4 : 0;
+#pragma unroll 2
+    for (int i = tid; i < quads; i += kSelThreads)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(key + 4 * i)), "l"(w + from + 4 * i)
+                   : "memory");
 #pragma unroll 4
-    for (int i = tid; i < cnt; i += kSelThreads)
+    for (int i = 4 * quads + tid; i < cnt; i += kSelThreads)
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(key + i)), "l"(w + from + i) : "memory");
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
@@ -402,7 +409,7 @@ static cudaError_t launch_select(const Cache8Evict& p, cudaStream_t st) {
 
 // evict, move: a CTA per (dst block, (b, KV head), K or V), eight to an SM (two dependent loads, a reduction and a
 // store have to overlap between CTAs: 137 MB of rows read and written in 23 us, 91% of the measured copy rate; the
-// whole eviction of 131072 -> 8192 tokens of 4 x 8 heads 52.7 us, 53.4 with six CTAs, 57.2 with four).  e4m3 magnitudes
+// whole eviction of 131072 -> 8192 tokens of 4 x 8 heads 52.7 us, 53.4 with six CTAs, 57.2 with four; now 51.4).  e4m3 magnitudes
 // order like their 7-bit codes, so the scale a row needs comes from its largest code and its old exponent, in integers.
 template <int D, int T>
 __global__ void __launch_bounds__(kThreads, 8) evict_move_kernel(const __grid_constant__ Cache8Evict p, int nblocks) {
