@@ -507,7 +507,11 @@ EVICTS = [  # B, Hkv, cap, d, block, keep, recent, dst capacity, lens
     (1, 8, 9000, 128, 128, 1100, 128, 1200, (9000,)),
     (2, 1, 300, 64, 128, 400, 7, 450, (300, 299)),
     (2, 1, 20000, 64, 64, 1500, 100, 1600, (20000, 17)),     # slices over a cluster of CTAs
-    (1, 1, 140000, 64, 128, 2000, 31, 2000, (139999,)),      # longer than the clusters' registers hold
+    (1, 1, 140000, 64, 128, 2000, 31, 2000, (139999,)),      # longer than the clusters' shared memory holds
+    # heads whose weights start at every remainder of 16 bytes
+    (2, 2, 333, 64, 64, 100, 9, 100, (333, 331)),
+    (1, 4, 20003, 64, 128, 700, 50, 700, (20003,)),
+    (1, 2, 131079, 64, 128, 300, 0, 300, (131079,)),
 ]
 
 
