@@ -616,6 +616,11 @@ def decode_attn(q, K_cache, V_cache, idx, *, scale: float = 0.0, o=None, lse=Non
     return o
 
 
+def _same(t) -> tuple:
+    """What a captured kernel takes of a tensor: where it lies and how it was checked."""
+    return t.data_ptr(), t.shape, t.dtype, t.is_contiguous()
+
+
 class FasaDecode:
     """One decode step for a fixed cache shape: TIP on the compact dominant-pair keys, top-k,
     focused attention.  ``fc`` [Hkv, nfc] are the dominant pairs (an input: the offline
@@ -666,16 +671,17 @@ class FasaDecode:
 
     def step(self, q, K_cache, V_cache=None, pos: int = -1):
         """One decode step for the token at position ``pos`` (its compact key row, select, attend)
-        replayed as a CUDA graph: captured on the first call for these buffers and this position,
-        replayed on later calls (new values in the same q / cache tensors are picked up; the
+        replayed as a CUDA graph: captured on the first call for these buffers (of a ``KvCache8``: all
+        that the kernels read) and this position, replayed on later calls (new values in the same q / cache tensors are picked up; the
         kernels, their arguments and the buffers are fixed at capture).  Runs on the current
         stream; returns ``self.o``."""
         if pos < 0:
             raise ValueError("step() needs the position of the newest token")
+        # Everything the captured kernels hold fixed, so that a graph never reads a buffer that is not this call's.
         if isinstance(K_cache, KvCache8):
-            key = (q.data_ptr(), K_cache.k.data_ptr(), K_cache.v.data_ptr(), K_cache.lens.data_ptr(), int(pos))
+            key = (int(pos), _same(q), K_cache._key)
         else:
-            key = (q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), int(pos))
+            key = (int(pos), _same(q), _same(K_cache), _same(V_cache))
         if getattr(self, "_graph_key", None) != key:
             side = torch.cuda.Stream(q.device)
             side.wait_stream(torch.cuda.current_stream(q.device))
@@ -745,6 +751,7 @@ class KvCache8:
         self._c = Cache8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), lens.data_ptr(),
                          None if weight is None else weight.data_ptr(), block)
         self._cref = ctypes.byref(self._c)
+        self._key = (*(x.data_ptr() for x in (k, v, k_scale, v_scale, lens)), tuple(k.shape), block)
         self._device, self._index = k.device, k.device.index
         self._shapes = {}  # heads_q -> (Shape, reference to it)
         self._kv_ref = self._shape_ref(Hkv)

@@ -692,3 +692,28 @@ def test_fasa_decode_on_the_8_bit_cache():
         m.step(qd, cache, pos=4999)
         assert torch.equal(m.idx, idx) and torch.equal(m.o, o)
     assert int(m.status.item()) == 0
+
+
+def test_graph_step_follows_the_cache_it_is_given():
+    """Caches over the same codes and lengths with other scales, and with other blocks: each step reads its own."""
+    rng = np.random.default_rng(61)
+    arr = Arrays(rng, 1, 2, 1000, 64, 64, (1000,), weight=False)
+    a = arr.gpu()
+    other = [torch.from_numpy(np.ldexp(x, rng.integers(-3, 4, x.shape)).astype(np.float32)).to(dev()) for x in (arr.ks, arr.vs)]
+    same = dict(k=a.k, v=a.v, lens=a.lens)
+    caches = [a, sfa.KvCache8(**same, k_scale=other[0], v_scale=a.v_scale, block=64),
+              sfa.KvCache8(**same, k_scale=a.k_scale, v_scale=other[1], block=64),
+              sfa.KvCache8(**same, k_scale=other[0][:, :, :8].contiguous(), v_scale=other[1][:, :, :8].contiguous())]
+    fc = np.tile(np.arange(8), (2, 1))
+    m, ref = (sfa.FasaDecode(batch=1, heads_q=8, heads_kv=2, seq_len=1000, head_dim=64, fc=fc, k=40) for _ in range(2))
+    q = bf16(rng.normal(size=(1, 8, 64))).to(dev())
+    outs = []
+    for c in caches + caches[::-1]:
+        for x in (m, ref):
+            x.refresh_keys(c)
+        got = m.step(q, c, pos=999)
+        want = ref(q, c)
+        assert torch.equal(got, want) and torch.equal(m.idx, ref.idx) and torch.equal(m.lse, ref.lse)
+        outs.append(want.clone())
+    assert not any(torch.equal(outs[0], o) for o in outs[1:4])
+    assert int(m.status.item()) == 0
