@@ -662,21 +662,29 @@ class FasaDecode:
         if isinstance(K_cache, KvCache8):
             cache8_attn_list(q, K_cache, self.idx, o=self.o, lse=self.lse, status=self.status, stream=stream)
             return
+        self._needs_values(K_cache, V_cache)
         decode_attn(q, K_cache, V_cache, self.idx, o=self.o, lse=self.lse, status=self.status, stream=stream)
 
+    @staticmethod
+    def _needs_values(K_cache, V_cache):
+        if V_cache is None and not isinstance(K_cache, KvCache8):
+            raise TypeError("V_cache is missing: a bf16 key cache comes with its value cache")
+
     def __call__(self, q, K_cache, V_cache=None, stream=None):
+        self._needs_values(K_cache, V_cache)
         self.select(q, stream)
         self.attend(q, K_cache, V_cache, stream)
         return self.o
 
-    def step(self, q, K_cache, V_cache=None, pos: int = -1):
+    def step(self, q, K_cache, V_cache=None, pos: int | None = None):
         """One decode step for the token at position ``pos`` (its compact key row, select, attend)
         replayed as a CUDA graph: captured on the first call for these buffers (of a ``KvCache8``: all
         that the kernels read) and this position, replayed on later calls (new values in the same q / cache tensors are picked up; the
         kernels, their arguments and the buffers are fixed at capture).  Runs on the current
         stream; returns ``self.o``."""
-        if pos < 0:
-            raise ValueError("step() needs the position of the newest token")
+        if pos is None:
+            raise TypeError("pos is missing: step() needs the position of the newest token")
+        self._needs_values(K_cache, V_cache)
         # Everything the captured kernels hold fixed, so that a graph never reads a buffer that is not this call's.
         if isinstance(K_cache, KvCache8):
             key = (int(pos), _same(q), K_cache._key)

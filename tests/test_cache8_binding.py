@@ -126,3 +126,27 @@ def test_a_step_checks_queries_of_another_shape_at_the_same_address(lib):
     m.step(big[:256].view(1, 4, 64), a, pos=3)
     with pytest.raises(ValueError, match="q must be"):
         m.step(big.view(1, 4, 128), a, pos=3)
+
+
+# ---------------------------------------------------------------------------
+# what the selecting decoder refuses
+# ---------------------------------------------------------------------------
+def test_a_missing_value_cache_or_position_is_named(lib):
+    m, x, K = decoder(), q(), torch.zeros((1, 2, 256, 64), dtype=torch.bfloat16)
+    for call in (lambda: m(x, K), lambda: m.attend(x, K), lambda: m.step(x, K, pos=3)):
+        with pytest.raises(TypeError, match="V_cache"):
+            call()
+    for call in (lambda: m.step(x, K, K), lambda: m.step(x, cache())):
+        with pytest.raises(TypeError, match="pos"):
+            call()
+    assert not lib.calls or {n for n, _ in lib.calls} == {"sfa_decode_workspace"}
+
+
+def test_a_position_before_the_cache_is_the_librarys_to_refuse(lib, monkeypatch):
+    """As for every other caller of the compact-key copy: SFA_ERR_INVALID_ARG, whichever cache is given."""
+    m, x, K = decoder(), q(), torch.zeros((1, 2, 256, 64), dtype=torch.bfloat16)
+    for name in ("sfa_decode_fc_gather", "sfa_cache8_fc_gather"):
+        monkeypatch.setattr(lib, name, lambda s, c, fc, nfc, pos0, *rest: 1 if pos0 < 0 else 0, raising=False)
+    for call in (lambda: m.step(x, K, K, -1), lambda: m.step(x, cache(), pos=-1)):
+        with pytest.raises(sfa.SfaError, match="SFA_ERR_INVALID_ARG"):
+            call()
