@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from ctypes import POINTER, c_double, c_float, c_int, c_int32, c_size_t, c_uint, c_void_p
 
 import torch
@@ -764,6 +765,7 @@ class KvCache8:
         self._shapes = {}  # heads_q -> (Shape, reference to it)
         self._kv_ref = self._shape_ref(Hkv)
         self._workspaces = {}
+        self._lock = threading.Lock()  # one host thread at a time between the launches of a call
 
     @classmethod
     def empty(cls, *, batch, heads_kv, capacity, head_dim, block=128, weight=True, device="cuda"):
@@ -821,12 +823,13 @@ class KvCache8:
     def attend(self, q, *, back=0, scale=0.0, accumulate=False, o=None, lse=None, stream=None):
         """Attention of q [B, Hq, d] or [B, Hq, nq, d] over the whole cache; ``accumulate`` adds the
         attention weights to ``weight`` (calls that do so follow each other: order streams yourself).
-        The handle keeps a workspace per stream."""
+        The handle keeps a workspace per stream; host threads may share it."""
         if accumulate and self.weight is None:
             raise ValueError("accumulate needs a cache with weights")
         w = self.weight if accumulate else None
-        return cache8_attn(q, self, back=back, scale=scale, o=o, lse=lse, weight_in=w, weight_out=w,
-                           workspace=self._workspace(q, accumulate, stream), status=self.status, stream=stream)
+        with self._lock:
+            return cache8_attn(q, self, back=back, scale=scale, o=o, lse=lse, weight_in=w, weight_out=w,
+                               workspace=self._workspace(q, accumulate, stream), status=self.status, stream=stream)
 
     def attend_list(self, q, idx, *, scale=0.0, o=None, lse=None, stream=None):
         """Attention of q [B, Hq, d] over the tokens of idx [B, Hq, k]; see cache8_attn_list."""
@@ -846,11 +849,11 @@ def cache8_append(cache: KvCache8, K, V, *, at=None, counts=None, status=None, s
     n = K.shape[2]
     dev, st = cache._launch(stream)
     rows, seqs = (cache.batch, cache.heads_kv, n, cache.head_dim), (cache.batch,)
-    _check(lib.sfa_cache8_append(cache._kv_ref, cache._cref,
-                                 _fits(K, "K", rows, torch.bfloat16, dev), _fits(V, "V", rows, torch.bfloat16, dev), n,
-                                 _fits(at, "at", seqs, torch.int32, dev),
-                                 _fits(counts, "counts", seqs, torch.int32, dev), cache._status_ptr(status), st),
-           "sfa_cache8_append")
+    with cache._lock:
+        _check(lib.sfa_cache8_append(cache._kv_ref, cache._cref, _fits(K, "K", rows, torch.bfloat16, dev),
+                                     _fits(V, "V", rows, torch.bfloat16, dev), n, _fits(at, "at", seqs, torch.int32, dev),
+                                     _fits(counts, "counts", seqs, torch.int32, dev), cache._status_ptr(status), st),
+               "sfa_cache8_append")
 
 
 def _cache8_query(q, cache: KvCache8):
@@ -873,7 +876,8 @@ def cache8_attn_workspace(q, cache: KvCache8, *, weights: bool = False) -> int:
 def cache8_attn(q, cache: KvCache8, *, back: int = 0, scale: float = 0.0, o=None, lse=None, weight_in=None,
                 weight_out=None, workspace=None, status=None, stream=None):
     """sfa_cache8_attn: attention of q [B, Hq, d] or [B, Hq, nq, d] (the newest nq tokens) over the whole
-    cache; returns o.  With ``weight_out`` every token's attention weight is added to ``weight_in``."""
+    cache; returns o.  With ``weight_out`` every token's attention weight is added to ``weight_in``.  A
+    ``workspace`` belongs to one call at a time, on the host as on the GPU."""
     lib = load()
     shape, nq = _cache8_query(q, cache)
     dev, st = cache._launch(stream)

@@ -359,7 +359,10 @@ sfa_status sfa_decode_attn(const sfa_shape* shape, const void* q, const void* K_
  *                     received so far (may be NULL where a call does not use it)
  * Rows at and after lens[b] are never read into a result and may hold anything.
  * lens and the other arrays must not change while a call's kernels run (calls on
- * one stream follow each other; order calls on several yourself).
+ * one stream follow each other; order calls on several yourself).  Some calls are
+ * two launches: host threads that share a stream must not be inside two calls at
+ * once that write the same cache, workspace or index list, or another call's
+ * launches fall between the two.
  * Shape rules: those of the decode calls above (dtype SFA_BF16; d in {64, 128};
  * heads_q / heads_kv in {1, 2, 4, 8}; batch * heads_kv * L < 2^31), block in
  * {64, 128} (SFA_ERR_SHAPE); any L >= 1.  A length or position found out of
@@ -421,7 +424,7 @@ size_t sfa_cache8_attn_workspace(const sfa_shape* shape, int nq, int weights);
  * A q element that is NaN or infinite makes its row's o NaN.
  * workspace: device, at least sfa_cache8_attn_workspace() bytes, 256-byte
  * aligned; nothing in it is kept between calls, and calls whose kernels overlap
- * on the GPU need one each.  A length outside [0, L] counts as 0.  A wait inside
+ * on the GPU, or that host threads make at the same time, need one each.  A length outside [0, L] counts as 0.  A wait inside
  * the kernel that runs out (about 2 s) sets SFA_ERR_TIMEOUT; the outputs are then
  * not valid.  Launches 2 kernels.
  */

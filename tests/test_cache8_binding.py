@@ -150,3 +150,44 @@ def test_a_position_before_the_cache_is_the_librarys_to_refuse(lib, monkeypatch)
     for call in (lambda: m.step(x, K, K, -1), lambda: m.step(x, cache(), pos=-1)):
         with pytest.raises(sfa.SfaError, match="SFA_ERR_INVALID_ARG"):
             call()
+
+
+# ---------------------------------------------------------------------------
+# host threads
+# ---------------------------------------------------------------------------
+def together(lib, name, word, calls):
+    """Runs the calls in a thread each; every library call `name` lasts a while.  The largest number of them that
+    were under way at once with the same `word` (an argument)."""
+    inside, most, guard = {}, [0], threading.Lock()
+
+    def slow(*args):
+        at = word(args)
+        with guard:
+            inside[at] = inside.get(at, 0) + 1
+            most[0] = max(most[0], inside[at])
+        time.sleep(0.02)
+        with guard:
+            inside[at] -= 1
+        return 0
+
+    setattr(lib, name, slow)
+    start = threading.Barrier(len(calls))
+    threads = [threading.Thread(target=lambda f=f: (start.wait(), f())) for f in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return most[0]
+
+
+def test_threads_never_share_the_handles_workspace(lib):
+    """An attention is two launches with the partial results of one in the workspace: a second thread's call on the
+    same stream must not get between them."""
+    c = cache()
+    assert together(lib, "sfa_cache8_attn", lambda args: args[10], [lambda: c.attend(q())] * 6) == 1
+
+
+def test_threads_append_one_after_the_other(lib):
+    """An append at the lengths is two launches, which read and then advance them."""
+    c, rows = cache(), torch.zeros((1, 2, 1, 64), dtype=torch.bfloat16)
+    assert together(lib, "sfa_cache8_append", lambda args: 0, [lambda: c.append(rows, rows)] * 6) == 1

@@ -717,3 +717,35 @@ def test_graph_step_follows_the_cache_it_is_given():
         outs.append(want.clone())
     assert not any(torch.equal(outs[0], o) for o in outs[1:4])
     assert int(m.status.item()) == 0
+
+
+def test_threads_share_a_handle():
+    """Four host threads on the default stream: attentions with partial results to join, and appended tokens."""
+    import threading
+
+    rng = np.random.default_rng(62)
+    arr = Arrays(rng, 1, 2, 6000, 128, 128, (6000,))
+    cache, grown = arr.gpu(), sfa.KvCache8.empty(batch=1, heads_kv=2, capacity=400, head_dim=128)
+    qs = [bf16(rng.normal(size=(1, 8, 128))).to(dev()) for _ in range(4)]
+    want = [cache.attend(q) for q in qs]
+    outs = [torch.zeros((100, 1, 8, 128), dtype=torch.bfloat16, device=dev()) for _ in qs]
+    rows = [torch.full((1, 2, 1, 128), float(i + 1), dtype=torch.bfloat16, device=dev()) for i in range(4)]
+    start = threading.Barrier(4)
+
+    def work(i):
+        start.wait()
+        for k in range(100):
+            cache.attend(qs[i], o=outs[i][k])
+            grown.append(rows[i], rows[i])
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w.expand_as(o))
+    held = co.values(codes(grown.k)[0, 0], grown.k_scale[0, 0].cpu().numpy(), 128)
+    assert grown.lens.tolist() == [400] and all((held[:, 0] == i + 1).sum() == 100 for i in range(4))
+    assert int(cache.status.item()) == 0 and int(grown.status.item()) == 0
