@@ -146,6 +146,20 @@ def _stream(stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _new(shape, dtype, device, stream, returned=True):
+    """A buffer for a call on ``stream`` (None: the current one).  It comes from that stream's memory, whose last
+    user is in front of the call there; from the current stream's, whatever is still queued on that one could write
+    to it while the call runs.  A buffer that the caller gets is not reused before the current stream is done with it
+    either."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return BF16
@@ -725,13 +739,6 @@ def _handle(stream):
     return stream.value if isinstance(stream, c_void_p) else stream
 
 
-def _fresh(t, stream):
-    """A buffer allocated for a call on ``stream``: its memory is not reused before that stream is done with it."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 class KvCache8:
     """Keys and values of ``B`` sequences in 8 bits (sfa_cache8 of include/sfa.h).
 
@@ -812,8 +819,8 @@ class KvCache8:
             return None
         key = (q.shape[1:-1], weights, _handle(self._launch(stream)[1]))
         if key not in self._workspaces:
-            self._workspaces[key] = _fresh(torch.empty(cache8_attn_workspace(q, self, weights=weights),
-                                                       dtype=torch.uint8, device=self.k.device), stream)
+            self._workspaces[key] = _new(cache8_attn_workspace(q, self, weights=weights), torch.uint8, self._device,
+                                         stream, returned=False)
         return self._workspaces[key]
 
     def append(self, K, V, *, at=None, counts=None, stream=None):
@@ -882,11 +889,11 @@ def cache8_attn(q, cache: KvCache8, *, back: int = 0, scale: float = 0.0, o=None
     shape, nq = _cache8_query(q, cache)
     dev, st = cache._launch(stream)
     sizes = q.shape
-    o = _fresh(torch.empty_like(q), stream) if o is None else o
+    o = _new(q.shape, q.dtype, dev, stream) if o is None else o
     tokens = (cache.batch, cache.heads_kv, cache.capacity)
     if workspace is None:
-        workspace = _fresh(torch.empty(cache8_attn_workspace(q, cache, weights=weight_out is not None),
-                                       dtype=torch.uint8, device=dev), stream)
+        workspace = _new(cache8_attn_workspace(q, cache, weights=weight_out is not None), torch.uint8, dev, stream,
+                         returned=False)
     nbytes = workspace.numel()
     _check(lib.sfa_cache8_attn(shape, cache._cref, _fits(q, "q", sizes, torch.bfloat16, dev), nq, back, scale,
                                _fits(o, "o", sizes, torch.bfloat16, dev),
@@ -905,7 +912,7 @@ def cache8_attn_list(q, cache: KvCache8, idx, *, scale: float = 0.0, o=None, lse
         raise ValueError("q must be [B, Hq, d] and idx [B, Hq, k]")
     shape, _ = _cache8_query(q, cache)
     dev, st = cache._launch(stream)
-    o = _fresh(torch.empty_like(q), stream) if o is None else o
+    o = _new(q.shape, q.dtype, dev, stream) if o is None else o
     rows, k = q.shape[:2], idx.shape[2]
     _check(lib.sfa_cache8_attn_list(shape, cache._cref, _fits(q, "q", q.shape, torch.bfloat16, dev),
                                     _fits(idx, "idx", (*rows, k), torch.int32, dev), k, scale,
@@ -934,7 +941,7 @@ def cache8_evict(src: KvCache8, dst: KvCache8, *, keep: int, recent: int = 0, id
     if dst.k.device != dev:
         raise ValueError(f"dst must be on {dev}, got {dst.k.device}")
     if idx is None:
-        idx = _fresh(torch.empty((src.batch, src.heads_kv, max(int(keep), 0)), dtype=torch.int32, device=dev), stream)
+        idx = _new((src.batch, src.heads_kv, max(int(keep), 0)), torch.int32, dev, stream)
     nbytes = 0 if workspace is None else workspace.numel()
     _check(lib.sfa_cache8_evict(src._kv_ref, src._cref, dst._cref, dst.capacity, keep, recent,
                                 _fits(idx, "idx", (src.batch, src.heads_kv, keep), torch.int32, dev),
@@ -953,7 +960,7 @@ def cache8_fc_gather(cache: KvCache8, fc, *, K_fc=None, pos0: int = 0, npos: int
     nfc = pairs.shape[1]
     dev, st = cache._launch(stream)
     rows = (cache.batch, cache.heads_kv, cache.capacity, 2 * nfc)
-    K_fc = _fresh(torch.empty(rows, dtype=torch.bfloat16, device=dev), stream) if K_fc is None else K_fc
+    K_fc = _new(rows, torch.bfloat16, dev, stream) if K_fc is None else K_fc
     npos = cache.capacity - pos0 if npos is None else npos
     _check(lib.sfa_cache8_fc_gather(cache._kv_ref, cache._cref, pairs.ctypes.data, nfc, pos0, npos,
                                     _fits(K_fc, "K_fc", rows, torch.bfloat16, dev), st), "sfa_cache8_fc_gather")

@@ -749,3 +749,38 @@ def test_threads_share_a_handle():
     held = co.values(codes(grown.k)[0, 0], grown.k_scale[0, 0].cpu().numpy(), 128)
     assert grown.lens.tolist() == [400] and all((held[:, 0] == i + 1).sum() == 100 for i in range(4))
     assert int(cache.status.item()) == 0 and int(grown.status.item()) == 0
+
+
+def segment_stream(t):
+    """The stream from whose memory the allocator made a tensor."""
+    at = t.data_ptr()
+    return next(s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= at < s["address"] + s["total_size"])
+
+
+def test_buffers_made_for_a_call_on_another_stream():
+    """Outputs and workspaces that a call makes come from its own stream's memory: what the current stream has still
+    to write to a block that was freed there does not reach them."""
+    rng = np.random.default_rng(63)
+    arr = Arrays(rng, 2, 2, 3000, 128, 128, (3000, 2000))
+    cache = arr.gpu()
+    q = bf16(rng.normal(size=(2, 8, 128))).to(dev())
+    idx = torch.randint(0, 2000, (2, 8, 64), dtype=torch.int32, device=dev())
+    fc = np.tile(np.arange(4), (2, 1))
+    small = [sfa.KvCache8.empty(batch=2, heads_kv=2, capacity=300, head_dim=128) for _ in range(2)]
+    calls = [lambda **kw: cache.attend(q, **kw), lambda **kw: sfa.cache8_attn(q, cache, **kw),
+             lambda **kw: cache.attend_list(q, idx, **kw), lambda **kw: sfa.cache8_fc_gather(cache, fc, **kw),
+             lambda **kw: cache.evict(small[len(kw)], keep=300, recent=20, **kw)]
+    want = [call() for call in calls]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call, w in zip(calls, want):
+        late = torch.empty_like(w)
+        torch.cuda._sleep(20_000_000)  # 10 ms before the current stream writes to the block that it frees here
+        late.view(torch.uint8).fill_(0x55)
+        del late
+        got = call(stream=side)
+        assert segment_stream(got) == side.cuda_stream
+        torch.cuda.synchronize()
+        assert torch.equal(got.view(torch.uint8), w.view(torch.uint8))  # (rows that hold nothing are NaN)
+    streams = {segment_stream(w) for w in cache._workspaces.values()}
+    assert streams == {torch.cuda.current_stream().cuda_stream, side.cuda_stream}
