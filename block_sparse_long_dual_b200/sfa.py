@@ -222,8 +222,7 @@ def make_shape(Q: torch.Tensor, K: torch.Tensor) -> Shape:
 def rope_table(base: float, seq_len: int, head_dim: int, device="cuda", stream=None):
     """cos/sin tables [seq_len, head_dim/2] float32 on ``device`` (sfa_rope_table)."""
     lib = load()
-    cos = torch.empty((seq_len, head_dim // 2), dtype=torch.float32, device=device)
-    sin = torch.empty_like(cos)
+    cos, sin = (_new((seq_len, head_dim // 2), torch.float32, device, stream) for _ in range(2))
     _check(lib.sfa_rope_table(float(base), seq_len, head_dim, _ptr(cos), _ptr(sin), _stream(stream)),
            "sfa_rope_table")
     return cos, sin
@@ -280,13 +279,13 @@ def block_scores(Q, K, cos, sin, *, band_split: int, block: int, flags: int = 0,
     if apply_rope and not store_q_rot:
         Q_rot = None
     elif apply_rope:
-        Q_rot = torch.empty_like(Q) if Q_rot is None else Q_rot
-        K_rot = torch.empty_like(K) if K_rot is None else K_rot
+        Q_rot = _new(Q.shape, Q.dtype, Q.device, stream) if Q_rot is None else Q_rot
+        K_rot = _new(K.shape, K.dtype, K.device, stream) if K_rot is None else K_rot
         _cuda(cos, "cos"); _cuda(sin, "sin")
     if probs is None:
-        probs = torch.empty((shape.batch, shape.heads_q, nb, nb), dtype=torch.float32, device=Q.device)
+        probs = _new((shape.batch, shape.heads_q, nb, nb), torch.float32, Q.device, stream)
     if workspace is None:
-        workspace = torch.empty(max(workspace_bytes(shape, block), 256), dtype=torch.uint8, device=Q.device)
+        workspace = _new(max(workspace_bytes(shape, block), 256), torch.uint8, Q.device, stream)
     _check_score_buffers(Q, K, cos, sin, apply_rope, Q_rot, K_rot, probs, workspace, nb)
     rope = Rope(cos.data_ptr() if apply_rope else None, sin.data_ptr() if apply_rope else None,
                 1 if apply_rope else 0)
@@ -311,18 +310,18 @@ def block_scores_select(Q, K, cos, sin, *, band_split: int, block: int, k: int |
     if apply_rope and not store_q_rot:
         Q_rot = None
     elif apply_rope:
-        Q_rot = torch.empty_like(Q) if Q_rot is None else Q_rot
-        K_rot = torch.empty_like(K) if K_rot is None else K_rot
+        Q_rot = _new(Q.shape, Q.dtype, Q.device, stream) if Q_rot is None else Q_rot
+        K_rot = _new(K.shape, K.dtype, K.device, stream) if K_rot is None else K_rot
         _cuda(cos, "cos"); _cuda(sin, "sin")
     if probs is None and want_probs:
-        probs = torch.empty((shape.batch, shape.heads_q, nb, nb), dtype=torch.float32, device=Q.device)
+        probs = _new((shape.batch, shape.heads_q, nb, nb), torch.float32, Q.device, stream)
     kmax = kmax_for(nb, k, flags) if kmax is None else kmax
     if counts is None:
-        counts = torch.empty((shape.batch, shape.heads_q, nb), dtype=torch.int32, device=Q.device)
+        counts = _new((shape.batch, shape.heads_q, nb), torch.int32, Q.device, stream)
     if idx is None:
-        idx = torch.empty((shape.batch, shape.heads_q, nb, max(kmax, 1)), dtype=torch.int32, device=Q.device)
+        idx = _new((shape.batch, shape.heads_q, nb, max(kmax, 1)), torch.int32, Q.device, stream)
     if workspace is None:
-        workspace = torch.empty(max(workspace_bytes(shape, block), 256), dtype=torch.uint8, device=Q.device)
+        workspace = _new(max(workspace_bytes(shape, block), 256), torch.uint8, Q.device, stream)
     _check_score_buffers(Q, K, cos, sin, apply_rope, Q_rot, K_rot, probs, workspace, nb)
     _expect(counts, "counts", (shape.batch, shape.heads_q, nb), torch.int32, Q.device)
     _expect(idx, "idx", (shape.batch, shape.heads_q, nb, idx.shape[-1]), torch.int32, Q.device)
@@ -356,9 +355,9 @@ def select(probs, shape: Shape, *, block: int, k: int | None = None, mass: float
     nb = shape.seq_len // block
     kmax = kmax_for(nb, k, flags) if kmax is None else kmax
     if counts is None:
-        counts = torch.empty((shape.batch, shape.heads_q, nb), dtype=torch.int32, device=probs.device)
+        counts = _new((shape.batch, shape.heads_q, nb), torch.int32, probs.device, stream)
     if idx is None:
-        idx = torch.empty((shape.batch, shape.heads_q, nb, kmax), dtype=torch.int32, device=probs.device)
+        idx = _new((shape.batch, shape.heads_q, nb, kmax), torch.int32, probs.device, stream)
     _expect(probs, "probs", (shape.batch, shape.heads_q, nb, nb), torch.float32)
     _expect(counts, "counts", (shape.batch, shape.heads_q, nb), torch.int32, probs.device)
     _expect(idx, "idx", (shape.batch, shape.heads_q, nb, kmax), torch.int32, probs.device)
@@ -389,7 +388,7 @@ def block_sparse_attn(Q, K, V, counts, idx, *, block: int, causal: bool = True, 
     shape = make_shape(Q, K)
     if V.shape != K.shape or V.dtype != K.dtype:
         raise ValueError("V must match K")
-    O = torch.empty_like(Q) if O is None else O
+    O = _new(Q.shape, Q.dtype, Q.device, stream) if O is None else O
     _check_attn_buffers(Q, K, V, counts, idx, O, lse, status, block)
     _check(lib.sfa_block_sparse_attn(ctypes.byref(shape), block, _ptr(Q), _ptr(K), _ptr(V), _ptr(counts),
                                      _ptr(idx), idx.shape[-1], 1 if causal else 0, float(scale), _ptr(O),
@@ -407,7 +406,7 @@ def block_sparse_attn_rope(Q, cos, sin, K_rot, V, counts, idx, *, block: int, ca
     shape = make_shape(Q, K_rot)
     if V.shape != K_rot.shape or V.dtype != K_rot.dtype:
         raise ValueError("V must match K_rot")
-    O = torch.empty_like(Q) if O is None else O
+    O = _new(Q.shape, Q.dtype, Q.device, stream) if O is None else O
     _expect(cos, "cos", (Q.shape[2], Q.shape[-1] // 2), torch.float32, Q.device)
     _expect(sin, "sin", (Q.shape[2], Q.shape[-1] // 2), torch.float32, Q.device)
     _check_attn_buffers(Q, K_rot, V, counts, idx, O, lse, status, block)
@@ -580,7 +579,7 @@ def decode_fc_gather(K_cache, fc, *, K_fc=None, pos0: int = 0, npos: int | None 
     fch, nfc = _fc_host(fc)
     shape = Shape(B, Hkv, Hkv, L, d, _dtype_code(K_cache))
     if K_fc is None:
-        K_fc = torch.empty((B, Hkv, L, 2 * nfc), dtype=K_cache.dtype, device=K_cache.device)
+        K_fc = _new((B, Hkv, L, 2 * nfc), K_cache.dtype, K_cache.device, stream)
     _expect(K_fc, "K_fc", (B, Hkv, L, 2 * nfc), K_cache.dtype, K_cache.device)
     npos = L - pos0 if npos is None else npos
     _check(lib.sfa_decode_fc_gather(ctypes.byref(shape), _ptr(K_cache), fch, nfc, pos0, npos, _ptr(K_fc),
@@ -596,10 +595,10 @@ def decode_select(q, K_fc, fc, L: int, *, k: int, idx=None, workspace=None, stat
     fch, nfc = _fc_host(fc)
     shape = Shape(B, Hq, K_fc.shape[1], L, d, _dtype_code(q))
     if idx is None:
-        idx = torch.empty((B, Hq, k), dtype=torch.int32, device=q.device)
+        idx = _new((B, Hq, k), torch.int32, q.device, stream)
     if workspace is None:
-        workspace = torch.empty(max(lib.sfa_decode_workspace(ctypes.byref(shape), k), 256), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _new(max(lib.sfa_decode_workspace(ctypes.byref(shape), k), 256), torch.uint8, q.device, stream,
+                         returned=False)
     _expect(K_fc, "K_fc", (B, K_fc.shape[1], L, 2 * nfc), q.dtype, q.device)
     _expect(idx, "idx", (B, Hq, k), torch.int32, q.device)
     _workspace(workspace)
@@ -616,7 +615,7 @@ def decode_attn(q, K_cache, V_cache, idx, *, scale: float = 0.0, o=None, lse=Non
     for t, n in ((q, "q"), (K_cache, "K_cache"), (V_cache, "V_cache"), (idx, "idx")):
         _cuda(t, n)
     shape = decode_shape(q, K_cache)
-    o = torch.empty_like(q) if o is None else o
+    o = _new(q.shape, q.dtype, q.device, stream) if o is None else o
     B, Hq, d = q.shape
     if K_cache.dim() != 4 or K_cache.shape[0] != B or K_cache.shape[3] != d:
         raise ValueError("K_cache must be [B, Hkv, L, d] matching q [B, Hq, d]")
