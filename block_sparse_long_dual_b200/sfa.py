@@ -491,12 +491,13 @@ class PrismAttention:
     def run_host(self, Q_host, K_host, V_host, O_host, dev_in=None, stream=None):
         """End to end from pinned host tensors: H2D copies, the path, D2H copy of O, all on one
         stream (each step's copies serialise with its kernels; HostPipeline overlaps them)."""
-        if dev_in is None:
-            dev_in = tuple(torch.empty(t.shape, dtype=t.dtype, device=self.O.device) for t in (Q_host, K_host, V_host))
-        for d, h in zip(dev_in, (Q_host, K_host, V_host)):
-            d.copy_(h, non_blocking=True)
-        self(*dev_in, stream=stream)
-        O_host.copy_(self.O, non_blocking=True)
+        with torch.cuda.stream(stream):  # (None: the current one)
+            if dev_in is None:
+                dev_in = tuple(torch.empty(t.shape, dtype=t.dtype, device=self.O.device) for t in (Q_host, K_host, V_host))
+            for d, h in zip(dev_in, (Q_host, K_host, V_host)):
+                d.copy_(h, non_blocking=True)
+            self(*dev_in)
+            O_host.copy_(self.O, non_blocking=True)
         return O_host
 
 
@@ -518,6 +519,7 @@ class HostPipeline:
         self.dev_out = [model.O, torch.empty_like(model.O)]
         self.up = torch.cuda.Stream(dev)
         self.down = torch.cuda.Stream(dev)
+        self.up.wait_stream(torch.cuda.current_stream(dev))  # the buffers' memory may still be written to there
         ev = lambda: [torch.cuda.Event() for _ in range(2)]
         self.in_ready, self.in_free, self.out_ready, self.out_free = ev(), ev(), ev(), ev()
         self.n = 0

@@ -70,3 +70,23 @@ def test_buffers_made_for_a_call_on_another_stream(name):
             here = torch.arange(a.shape[-1], device=a.device) < n[..., None]
             a, b = torch.where(here, a, -1), torch.where(here, b, -1)
         assert torch.equal(a, b)
+
+
+def test_a_step_from_host_memory_runs_on_the_stream_it_is_given():
+    """Its copies too: a busy current stream does not hold them up, nor let them overtake the kernels."""
+    g = torch.Generator().manual_seed(6)
+    host = [torch.randn((1, h, 1024, 128), generator=g).bfloat16().pin_memory() for h in (4, 2, 2)]
+    m = sfa.PrismAttention(batch=1, heads_q=4, heads_kv=2, seq_len=1024, head_dim=128, dtype="bf16", block=128,
+                           rope_base=10000.0, band_split=32, k=3)
+    out, want = (torch.zeros((1, 4, 1024, 128), dtype=torch.bfloat16).pin_memory() for _ in range(2))
+    m.run_host(*host, want)
+    torch.cuda.synchronize()
+    m.O.zero_()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(1_000_000_000)  # half a second
+    m.run_host(*host, out, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want)
+    assert not torch.cuda.current_stream().query()  # the current stream is still busy
+    torch.cuda.synchronize()
