@@ -924,7 +924,7 @@ def cache8_attn_list(q, cache: KvCache8, idx, *, scale: float = 0.0, o=None, lse
 
 
 def cache8_evict_workspace(src: KvCache8, keep: int) -> int:
-    """Bytes of workspace cache8_evict needs."""
+    """Bytes of workspace cache8_evict needs where it is given one instead of idx."""
     n = int(load().sfa_cache8_evict_workspace(src._kv_ref, int(keep)))
     if n == 0:
         raise SfaError(1, "sfa_cache8_evict_workspace")
@@ -934,20 +934,23 @@ def cache8_evict_workspace(src: KvCache8, keep: int) -> int:
 def cache8_evict(src: KvCache8, dst: KvCache8, *, keep: int, recent: int = 0, idx=None, workspace=None, status=None,
                  stream=None):
     """sfa_cache8_evict: the last ``recent`` tokens and those of the largest ``src.weight``, ``keep`` in all,
-    move to ``dst``; returns idx [B, Hkv, keep] int32, their rows in src (ascending, -1 padded)."""
+    move to ``dst``; returns idx [B, Hkv, keep] int32, their rows in src (ascending, -1 padded).  Without ``idx``
+    the list lies in ``workspace`` (the returned list is a view of it) or, without that too, in a new tensor."""
     lib = load()
     dev, st = src._launch(stream)
     if (dst.batch, dst.heads_kv, dst.head_dim) != (src.batch, src.heads_kv, src.head_dim):
         raise ValueError("dst must have the batch, heads and head dim of src")
     if dst.k.device != dev:
         raise ValueError(f"dst must be on {dev}, got {dst.k.device}")
-    if idx is None:
+    if idx is None and workspace is None:
         idx = _new((src.batch, src.heads_kv, max(int(keep), 0)), torch.int32, dev, stream)
     nbytes = 0 if workspace is None else workspace.numel()
     _check(lib.sfa_cache8_evict(src._kv_ref, src._cref, dst._cref, dst.capacity, keep, recent,
                                 _fits(idx, "idx", (src.batch, src.heads_kv, keep), torch.int32, dev),
                                 _fits(workspace, "workspace", (nbytes,), torch.uint8, dev), nbytes,
                                 src._status_ptr(status), st), "sfa_cache8_evict")
+    if idx is None:
+        idx = workspace[:4 * src.batch * src.heads_kv * keep].view(torch.int32).view(src.batch, src.heads_kv, keep)
     return idx
 
 

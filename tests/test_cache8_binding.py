@@ -191,3 +191,24 @@ def test_threads_append_one_after_the_other(lib):
     """An append at the lengths is two launches, which read and then advance them."""
     c, rows = cache(), torch.zeros((1, 2, 1, 64), dtype=torch.bfloat16)
     assert together(lib, "sfa_cache8_append", lambda args: 0, [lambda: c.append(rows, rows)] * 6) == 1
+
+
+# ---------------------------------------------------------------------------
+# the eviction's list
+# ---------------------------------------------------------------------------
+def evicting(keep=5, **kw):
+    src = sfa.KvCache8.empty(batch=1, heads_kv=2, capacity=256, head_dim=64, device="cpu")
+    dst = sfa.KvCache8.empty(batch=1, heads_kv=2, capacity=64, head_dim=64, device="cpu")
+    return sfa.cache8_evict(src, dst, keep=keep, **kw)
+
+
+def test_an_eviction_without_a_list_works_in_the_workspace_it_is_given(lib):
+    ws = torch.zeros(255, dtype=torch.uint8)
+    got = evicting(workspace=ws)
+    name, args = lib.calls[-1]
+    assert name == "sfa_cache8_evict" and args[6] is None and args[7] == ws.data_ptr() and args[8] == 255
+    assert got.shape == (1, 2, 5) and got.dtype == torch.int32 and got.data_ptr() == ws.data_ptr()
+    idx = torch.zeros((1, 2, 5), dtype=torch.int32)
+    assert evicting(idx=idx, workspace=ws) is idx and lib.calls[-1][1][6] == idx.data_ptr()
+    own = evicting()
+    assert lib.calls[-1][1][6] == own.data_ptr() and own.shape == (1, 2, 5)

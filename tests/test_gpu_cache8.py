@@ -784,3 +784,20 @@ def test_buffers_made_for_a_call_on_another_stream():
         assert torch.equal(got.view(torch.uint8), w.view(torch.uint8))  # (rows that hold nothing are NaN)
     streams = {segment_stream(w) for w in cache._workspaces.values()}
     assert streams == {torch.cuda.current_stream().cuda_stream, side.cuda_stream}
+
+
+def test_eviction_with_its_list_in_the_workspace():
+    rng = np.random.default_rng(64)
+    arr = Arrays(rng, 2, 2, 700, 64, 64, (700, 90), behind=False)
+    src = arr.gpu()
+    empty = [Arrays(rng, 2, 2, 128, 64, 64, (0, 0), behind=False).gpu() for _ in range(2)]
+    ws = torch.full((sfa.cache8_evict_workspace(src, 100),), 0x55, dtype=torch.uint8, device=dev())
+    idx = sfa.cache8_evict(src, empty[0], keep=100, recent=10, workspace=ws)
+    want = src.evict(empty[1], keep=100, recent=10)
+    assert idx.data_ptr() == ws.data_ptr() and torch.equal(idx, want)
+    for b in range(2):
+        n = int(empty[0].lens[b])
+        assert n == min(100, int(arr.lens[b]))
+        assert torch.equal(empty[0].k[b, :, :n].view(torch.uint8), empty[1].k[b, :, :n].view(torch.uint8))
+    with pytest.raises(sfa.SfaError, match="WORKSPACE"):
+        sfa.cache8_evict(src, empty[0], keep=100, recent=10, workspace=ws[:1536])
