@@ -1,5 +1,6 @@
 // 8-bit KV cache: e4m3 codes, power-of-two block scales, and how a call's work
-// is split over CTAs.  Shared by cache8_store.cu and cache8_attn.cu.
+// is split over CTAs.  Shared by cache8_store.cu, cache8_attn.cu, cache8_attn_tc.cu and
+// api.cu.
 #pragma once
 
 #include <cuda.h>
@@ -196,7 +197,7 @@ __device__ __forceinline__ int warp_share(const int* lens, int B, int Hkv, int L
 }  // namespace c8
 
 // ---------------------------------------------------------------------------
-// Launch interface (cache8_api.cu -> kernels)
+// Launch interface (api.cu -> kernels)
 // ---------------------------------------------------------------------------
 struct Cache8Append {
   const void* K;

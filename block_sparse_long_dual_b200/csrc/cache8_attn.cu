@@ -26,14 +26,16 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Launched while the first step still runs: everything up to pieces_ready() needs
 // only the lengths.  At 16 x 8 units of 4 rows over 32768 tokens it adds 4 us to the
 // 160 of the first step; with weights, 4 x 8 units over 131072 tokens, 21 us for
-// 67 MB of scores, 17 of weights read and 17 written: 4.8 TB/s.
+// 67 MB of scores, 17 of weights read and 17 written: 4.8 TB/s.  With 16 rows the
+// scores are 128 bytes a token, written and read: 16 x 8 units over 16384 tokens cost
+// 58 us more than without weights at d = 128 (151 against 93), 51 at d = 64 (122, 71).
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
 __device__ __forceinline__ void pieces_ready() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Tokens per thread of the weights part: about four 16-byte loads of scores in flight (128K x 4 with weights: the
-// whole call 201.5 us, 204.5 with eight, which spill).
+// whole call 201.5 us, 204.5 with eight, which spill; of the four, 4 to 8 bytes a thread spill where CTAs join by rows).
 constexpr int weight_tokens(int CP) { return CP <= 4 ? 4 : (CP == 8 ? 2 : 1); }
 
 template <int D, int CP, bool UNIT>  // CP = p.cpad; UNIT: a joining CTA takes all rows of a unit

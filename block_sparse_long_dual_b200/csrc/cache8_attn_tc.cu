@@ -7,10 +7,16 @@
 //   O^T [D, 2 NC]          = V^T [D, 128] . P^T
 // A bf16 query row or a float32 probability does not fit 4 significant bits, so
 // each takes two columns: x = hi + lo / 2^k, hi = e4m3(x), lo = e4m3((x - hi) 2^k).
-// For a query row scaled to its largest element, hi and lo together hold every
-// bf16 significand exactly down to 2^-21 of the largest; for probabilities scaled
-// to their block's largest, 8 significant bits down to 2^-14 and an absolute step
-// of 2^-23.  The products' sums, scores, maxima, sums and O are float32.
+// A query row is scaled so that its largest element lies in (224, 448]; with k = 4 the
+// two parts end at steps of 2^-13, so a bf16 element of at least 2^-6 (2^-13 of the
+// largest is always enough) is exact and a smaller one off by 2^-14 at most, under
+// 2^-21 of the largest.  Probabilities are scaled to 256 for their block's largest; with
+// k = 5 the parts are off by 2^-9 of the value at most (the width of bf16), or by half a
+// step of 2^-22 of the block's largest where that is more.  The rounding is unbiased and
+// only O sees it: the sum that divides O, lse and the weights take the probabilities as
+// computed.  It brings O's error against 64 bits from 1.67e-3 (the bf16 output's own
+// rounding) to 1.73e-3, over 32768 tokens of normal values.  (A third part would take a
+// stage of the rings at d 64.)  The products' sums, scores, maxima, sums and O are float32.
 //
 // Each scale block has its own reference maximum and, in TMEM, its own O^T, so
 // scales that lie far apart between blocks lose nothing: the block's factor
@@ -29,10 +35,11 @@
 // N = 2 NC; the tensor core is idle most of the time and the kernel's bound is the
 // cache's bytes: 16 x 8 heads x 32768 tokens, d 128, 4 rows: 160 us for 1074 MB, 6.7
 // TB/s (102% of the measured copy rate, which writes half its bytes); d 64 with 8 rows
-// 5.0 - 5.3 TB/s, bound by the softmax warps.  Work split, pieces and their slots: cache8.cuh.  Every wait is
-// bounded; one that runs out sets SFA_ERR_TIMEOUT and an abort flag, after which
-// waits return at once and the CTA runs to its end (the copies and MMAs it issued
-// are drained).
+// 5.0 - 5.3 TB/s and with 16 rows 3.8, bound by the softmax warps.  144 to 168 registers;
+// 16 rows of d 64 over 64-token blocks spill 12 bytes a thread.  Work split, pieces and
+// their slots: cache8.cuh.  Every wait is bounded; one that runs out sets
+// SFA_ERR_TIMEOUT and an abort flag, after which waits return at once and the CTA runs
+// to its end (the copies and MMAs it issued are drained).
 #include <cuda.h>
 #include <float.h>
 #include <math.h>
@@ -775,7 +782,8 @@ __global__ void __launch_bounds__(kTileThreads, kCtasPerSm)
           __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.o) + (size_t)unit * p.cols * D + tid;
 #pragma unroll
           for (int c = 0; c < NC; ++c)
-            if (c < p.cols)  // sum = 0 exactly when the row sees no token (a NaN score makes it NaN, and the row's o)
+            if (c < p.cols)  // sum = 0 exactly when the row sees no token (a NaN score makes it NaN, and the row's o);
+                             // the division is 2 ulp of float32 off at most, for sums under 2^31
               to[c * D] = __float2bfloat16_rn(sum[c] == 0.f ? 0.f : __fdividef(o[c], sum[c]));
         }
         if (!more) break;
@@ -802,7 +810,7 @@ cudaError_t launch_t(const Cache8Attn& p, const CUtensorMap& tk, const CUtensorM
   using L = Lay<D, NC, T>;
   static_assert(kCtasPerSm * (L::BYTES + 1024) <= 228 * 1024, "shared memory of an SM");
   static_assert(kCtasPerSm * L::TMEM <= 512, "tensor memory of an SM");
-  static_assert(L::SUB * NC <= 32, "a lane of warp 0 for each factor");
+  static_assert(L::SUB * NC <= 32, "a lane of warp 4 for each factor");
   auto kern = attn_tile_kernel<D, NC, T>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem_once(kern, L::BYTES, true, done);

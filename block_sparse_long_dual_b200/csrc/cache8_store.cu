@@ -157,8 +157,8 @@ __global__ void advance_kernel(Cache8Append p) {
 // that runs once waits for its instructions (keys in registers: 7 us more).
 // One histogram serves: with two or four copies, lanes apart, 53.5 and 55.5 us
 // against 53.3, with equal weights everywhere 57.5 against 57.2.
-// 131072 -> 8192 tokens of 4 x 8 heads (the times above are this whole eviction's):
-// the selection takes 25 us for 17 MB, bound by the latencies of its steps
+// 131072 -> 8192 tokens of 4 x 8 heads (the times above are this whole eviction's,
+// now 52 us): the selection takes 25 us for 17 MB, bound by the latencies of its steps
 // (histograms 6 us, meetings and sums 9, the copy 3, the list 2).
 // ---------------------------------------------------------------------------
 constexpr int kSlice = 16384;  // keys in shared memory
@@ -409,8 +409,9 @@ static cudaError_t launch_select(const Cache8Evict& p, cudaStream_t st) {
 
 // evict, move: a CTA per (dst block, (b, KV head), K or V), eight to an SM (two dependent loads, a reduction and a
 // store have to overlap between CTAs: 137 MB of rows read and written in 23 us, 91% of the measured copy rate; the
-// whole eviction of 131072 -> 8192 tokens of 4 x 8 heads 52.7 us, 53.4 with six CTAs, 57.2 with four; now 51.4).  e4m3 magnitudes
-// order like their 7-bit codes, so the scale a row needs comes from its largest code and its old exponent, in integers.
+// whole eviction of 131072 -> 8192 tokens of 4 x 8 heads 52.7 us when it was tried, 53.4 with six CTAs, 57.2 with four).
+// Eight CTAs leave 32 registers a thread: d 128 with 128-token blocks spills 16 bytes of them.  e4m3 magnitudes order
+// like their 7-bit codes, so the scale a row needs comes from its largest code and its old exponent, in integers.
 template <int D, int T>
 __global__ void __launch_bounds__(kThreads, 8) evict_move_kernel(const __grid_constant__ Cache8Evict p, int nblocks) {
   constexpr int CPR = D / 16;             // 16-byte chunks per row
@@ -486,7 +487,8 @@ __global__ void __launch_bounds__(kThreads, 8) evict_move_kernel(const __grid_co
 // sector of a row, so whole rows are read, 16 bytes a lane, and staged in shared memory (row stride
 // D + 4 bytes: the byte reads of neighbouring tokens fall into different banks); the output leaves
 // four bytes (two columns) a thread, contiguous over the CTA's tokens.  131072 tokens x 4 x 8 heads, 12 pairs, d 128:
-// 537 MB read and 201 MB written in 124 us, 5.9 TB/s, 91% of the measured copy rate: bound by those bytes.
+// 537 MB read and 201 MB written in 124 us replayed in a graph, 5.9 TB/s (91% of the measured copy rate), in 126 to 140
+// us called from Python: bound by those bytes, and by 74% of the issue slots beside them.
 // ---------------------------------------------------------------------------
 constexpr int kGatherTokens = 128;
 
@@ -556,7 +558,11 @@ cudaError_t launch_cache8_append(const Cache8Append& p, cudaStream_t st) {
 cudaError_t launch_cache8_evict(const Cache8Evict& p, cudaStream_t st) {
   if ((long long)p.B * p.Hkv * 8 >= (1LL << 31)) return cudaErrorInvalidValue;
   // One CTA's shared memory holds 16384 keys; longer caches are spread over eight CTAs a head, of half the threads
-  // (two share an SM, and every warp pays for the meetings: 131072 tokens 32 against 40 us).
+  // (two share an SM, and every warp pays for the meetings: 131072 tokens 32 against 40 us).  The host knows the
+  // capacity, not the lengths, so the rule is on the capacity.  Whole evictions to 8192 tokens of 4 x 8 heads, one CTA
+  // a head against eight: 16384 tokens 36.1, 40.4 us; 32768 55.1, 43.6; 131072 126.7, 52.5.  It costs a long cache
+  // that holds little: 2175 -> 2048 tokens of 16 x 8 heads 29.8 us in a cache of 2304 rows, 78.7 in one of 131072
+  // (30.6 with one CTA a head).
   cudaError_t e = p.L > kSlice ? launch_select<8, 512>(p, st) : launch_select<1, 1024>(p, st);
   if (e != cudaSuccess) return e;
   const int most = p.keep < p.L ? p.keep : p.L;

@@ -422,6 +422,12 @@ size_t sfa_cache8_attn_workspace(const sfa_shape* shape, int nq, int weights);
  * Other elements of weight_out are left alone.  The sums have a fixed order:
  * the same call gives the same bits.
  * A q element that is NaN or infinite makes its row's o NaN.
+ * Precision: a query row is used as two 8-bit parts, exact for elements of at
+ * least 2^-13 of the row's largest magnitude, others off by at most 2^-21 of it.
+ * In the sum over v_t a probability counts as two 8-bit parts, off by at most
+ * 2^-9 of its value (as a bf16 would be) or 2^-23 of the largest in its scale
+ * block, whichever is more; the sum that divides o, lse and the weights take it
+ * as computed (float32, hardware exp2).
  * workspace: device, at least sfa_cache8_attn_workspace() bytes, 256-byte
  * aligned; nothing in it is kept between calls, and calls whose kernels overlap
  * on the GPU, or that host threads make at the same time, need one each.  A length outside [0, L] counts as 0.  A wait inside
@@ -468,8 +474,9 @@ sfa_status sfa_cache8_evict(const sfa_shape* shape, const sfa_cache8* src, const
 
 /*
  * sfa_decode_fc_gather from the 8-bit cache: K_fc [B, heads_kv, L, 2 nfc] bf16
- * rows [pos0, pos0 + npos) from the cached keys' values (exact in bf16, so a
- * selection on K_fc ranks the keys that the attention reads).  Rows are copied
+ * rows [pos0, pos0 + npos) from the cached keys' values (exact in bf16 under
+ * scales of 2^-124 and more, so a selection on K_fc ranks the keys that the
+ * attention reads).  Rows are copied
  * whether or not they lie below lens[b].  fc, nfc, errors as sfa_decode_fc_gather.
  */
 sfa_status sfa_cache8_fc_gather(const sfa_shape* shape, const sfa_cache8* cache, const int* fc,
