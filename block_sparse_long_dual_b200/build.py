@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libsfa.so")
 SOURCES = ["api.cu", "scores.cu", "scores_noalloc.cu", "select.cu", "attn_simt.cu", "attn_tc.cu", "decode.cu",
            "cache8_store.cu", "cache8_attn.cu", "cache8_attn_tc.cu",
            "selftest.cu"]
-HEADERS = ["common.cuh", "kernels.h", "tc_ptx.cuh", "select_row.cuh", "cache8.cuh"]
+HEADERS = ["common.cuh", "kernels.h", "tc_ptx.cuh", "select_row.cuh", "cache8.cuh", "tc_ptx8.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -4,7 +4,7 @@
 #include <math.h>
 
 #include "cache8.cuh"
-#include "tc_ptx.cuh"
+#include "tc_ptx8.cuh"
 
 namespace sfa {
 

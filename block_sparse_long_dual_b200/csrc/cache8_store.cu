@@ -3,7 +3,7 @@
 #include <cooperative_groups.h>
 
 #include "cache8.cuh"
-#include "tc_ptx.cuh"
+#include "tc_ptx8.cuh"
 
 namespace sfa {
 

@@ -69,3 +69,10 @@ def test_scoring_bytes_without_stored_q_rot_or_probs(bench):
     assert bench.scoring_bytes(w, True, False) == (q + k) + k + table + means + probs
     assert bench.scoring_bytes(w, False, True) == 2 * (q + k) + table + means
     assert bench.scoring_bytes(w, False, False) == (q + k) + k + table + means
+
+
+def test_traffic_record_belongs_to_the_present_attention_kernel():
+    """The bench line's DRAM traffic is tied to the kernel's sources: a change to them needs another capture."""
+    import bench
+    rec = bench.traffic_record("block_sparse_long_dual_b200/csrc/attn_tc.cu")
+    assert rec is not None and rec["bytes_per_launch"] > 0
