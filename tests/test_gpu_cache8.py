@@ -801,3 +801,24 @@ def test_eviction_with_its_list_in_the_workspace():
         assert torch.equal(empty[0].k[b, :, :n].view(torch.uint8), empty[1].k[b, :, :n].view(torch.uint8))
     with pytest.raises(sfa.SfaError, match="WORKSPACE"):
         sfa.cache8_evict(src, empty[0], keep=100, recent=10, workspace=ws[:1536])
+
+
+def test_weights_without_earlier_ones_and_eviction_into_a_cache_without():
+    """weight_out alone starts from zero; a destination that keeps no weights gets the rows all the same."""
+    rng = np.random.default_rng(65)
+    arr = Arrays(rng, 2, 2, 500, 64, 64, (500, 77))
+    cache = arr.gpu()
+    q = bf16(rng.normal(size=(2, 4, 2, 64)))
+    w = torch.full(arr.w.shape, 7.0, device=dev())
+    o = sfa.cache8_attn(q.to(dev()), cache, weight_out=w)
+    arr.w = np.zeros_like(arr.w)
+    lse = torch.empty((2, 4, 2), device=dev())
+    assert torch.equal(o, cache.attend(q.to(dev()), lse=lse))
+    check_attn(arr, q, 2, 0, o, lse, w)
+    with_w, without = (sfa.KvCache8.empty(batch=2, heads_kv=2, capacity=90, head_dim=64, block=64, weight=x)
+                       for x in (True, False))
+    assert torch.equal(cache.evict(with_w, keep=80, recent=9), cache.evict(without, keep=80, recent=9))
+    for name in ("k", "v", "k_scale", "v_scale", "lens"):
+        a, b = (getattr(c, name).view(torch.uint8) for c in (with_w, without))
+        assert torch.equal(a, b)
+    assert int(cache.status.item()) == 0
